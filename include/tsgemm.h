@@ -45,6 +45,10 @@ typedef struct tsgemm_plan tsgemm_plan; /* opaque, owned by the library */
 /* TSGEMM_MXFP8: block-scaled FP8 inputs with bf16 output (tsgemm_run_mx). */
 enum { TSGEMM_FP16 = 1, TSGEMM_BF16 = 2, TSGEMM_MXFP8 = 3 };
 
+/* A further element type of the activations, weights and gradients of
+ * tsgemm_layer_norm and the calls after it. */
+enum { TSGEMM_FP32 = 4 };
+
 enum {
     TSGEMM_OK = 0,
     TSGEMM_EINVAL = -1,       /* malformed argument                              */
@@ -248,6 +252,73 @@ int tsgemm_run_mx_packed(const tsgemm_plan* plan, const void* A, const void* SFA
  *   without ordering between them) race on it. */
 int tsgemm_run_mx_noalloc(const tsgemm_plan* plan, const void* A, const void* SFA, const void* B,
                           const void* SFB, void* C, void* stream);
+
+/* ---- what a normalised linear layer needs around the MXFP8 product --------
+ *
+ * Matrices are row-major; of floating-point ones the distance between rows is
+ * an argument (elements, at least the width), and pointers need the alignment
+ * of their type unless said otherwise.  MX activations are laid out as A and
+ * SFA of tsgemm_run_mx: codes uint8[rows][width] (16-byte aligned), scales
+ * uint8[rows][width/32] (4-byte aligned), width % 32 == 0.  All pointers are
+ * DEVICE pointers owned by the caller, outputs must not overlap inputs, and
+ * every call only enqueues work on `stream`.  Sums and statistics are fp32;
+ * a result is rounded once, to nearest, ties to even.
+ *
+ * tsgemm_layer_norm: for every row of x
+ *     mean = sum(x) / width      rstd = (sum((x - mean)^2) / width + eps)^(-1/2)
+ *     y    = (x - mean) * rstd * gamma + beta
+ *   x and y are of `dtype` (TSGEMM_FP16, TSGEMM_BF16 or TSGEMM_FP32); gamma and
+ *   beta (NULL: ones, zeros) of `weight_dtype`, which is dtype or TSGEMM_FP32.
+ *   Outputs: y, or codes and scales (y held as MX, without a rounding to dtype
+ *   before), or both; mean and rstd (fp32[rows]) together or not at all.
+ *   width >= 1; eps finite, >= 0; rows == 0 launches nothing. */
+int tsgemm_layer_norm(int64_t rows, int64_t width, int dtype, int weight_dtype, const void* x, int64_t ldx,
+                      const void* gamma, const void* beta, float eps, void* y, int64_t ldy, float* mean,
+                      float* rstd, void* codes, void* scales, void* stream);
+
+/* The gradient of tsgemm_layer_norm: with h = (x - mean) * rstd, g = dy * gamma
+ *     dx     = rstd * (g - sum(g) / width - h * sum(g * h) / width)   per row
+ *     dgamma = sum over rows of dy * h      dbeta = sum over rows of dy
+ *   dy, x and dx are of `dtype`, gamma, dgamma and dbeta of `weight_dtype`;
+ *   mean and rstd as tsgemm_layer_norm wrote them.  dgamma or dbeta may be
+ *   NULL (not wanted).  The sums over rows are taken in a fixed order, the same
+ *   for every call of a shape.  They need `workspace` (16-byte aligned, at
+ *   least tsgemm_layer_norm_grad_workspace bytes, contents irrelevant; not
+ *   needed when both are NULL).  rows == 0 makes dgamma and dbeta zero. */
+int64_t tsgemm_layer_norm_grad_workspace(int64_t rows, int64_t width);
+int tsgemm_layer_norm_grad(int64_t rows, int64_t width, int dtype, int weight_dtype, const void* dy, int64_t lddy,
+                           const void* x, int64_t ldx, const void* gamma, const float* mean, const float* rstd,
+                           void* dx, int64_t lddx, void* dgamma, void* dbeta, void* workspace,
+                           int64_t workspace_bytes, void* stream);
+
+/* Activations to MX and back (OCP Microscaling Formats specification v1.0).
+ * Quantize: per 32 values along a row the scale is 2^(floor(log2 max|x|) - 8)
+ *   (its code that exponent + 127, at least 0, 0 too for a block of zeros), the
+ *   codes x / scale rounded to E4M3 and held at +-448.  A NaN or infinite value
+ *   becomes a NaN code; the scale is then that of the block's finite values.
+ * Dequantize: code * scale, rounded once to `dtype` (exact in TSGEMM_FP32 and,
+ *   where no value is below 2^-126, in TSGEMM_BF16); a NaN code or scale gives
+ *   NaN, a value past the type's range an infinity.
+ * rows * width == 0 launches nothing. */
+int tsgemm_mx_quantize(int64_t rows, int64_t width, int dtype, const void* x, int64_t ldx, void* codes, void* scales,
+                       void* stream);
+int tsgemm_mx_dequantize(int64_t rows, int64_t width, int dtype, const void* codes, const void* scales, void* out,
+                         int64_t ldo, void* stream);
+
+/* The weight gradient of a linear layer from its MX activation:
+ *     dw[o][i] = sum_r dy[r][o] * code[r][i] * scale[r][i/32]
+ *   dy[rows][out] is TSGEMM_FP16 or TSGEMM_BF16 (`dtype`), its rows 16-byte
+ *   aligned (out % 8 == 0, lddy % 8 == 0); dw[out][width] is contiguous, 16-byte
+ *   aligned, of dtype or TSGEMM_FP32 (`grad_dtype`).  The terms keep all bits
+ *   of both factors; the sum is fp32.  Shapes with few tiles of dw split the
+ *   rows over workgroups and need `workspace` (16-byte aligned,
+ *   tsgemm_mx_weight_grad_workspace bytes, possibly 0); the result of a shape
+ *   is the same bits every time.  rows == 0 makes dw zero, out * width == 0
+ *   launches nothing. */
+int64_t tsgemm_mx_weight_grad_workspace(int64_t rows, int64_t out, int64_t width);
+int tsgemm_mx_weight_grad(int64_t rows, int64_t out, int64_t width, int dtype, int grad_dtype, const void* dy,
+                          int64_t lddy, const void* codes, const void* scales, void* dw, void* workspace,
+                          int64_t workspace_bytes, void* stream);
 
 /* m_blocks * n_blocks, the tile count the scheduler walks (page "[Feature]
  * Introduce tile scheduler #2441", Files changed: the waves formula

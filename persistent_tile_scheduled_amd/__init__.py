@@ -7,7 +7,9 @@ and fails loudly otherwise.
 
 Names follow the C ABI: ``create`` -> :class:`Plan`, ``Plan.run``,
 ``Plan.run_traced``, ``Plan.run_mx``, ``Plan.run_mx_traced``,
-``Plan.dump_schedule``, ``Plan.schedule_host``, ``Plan.info``, ``last_error``.
+``Plan.dump_schedule``, ``Plan.schedule_host``, ``Plan.info``, ``last_error``,
+``layer_norm``, ``layer_norm_grad``, ``mx_quantize``, ``mx_dequantize``,
+``mx_weight_grad``.
 """
 
 from __future__ import annotations
@@ -25,6 +27,7 @@ LIB_PATH = os.path.join(_HERE, "libtsgemm.so")
 FP16 = 1
 BF16 = 2
 MXFP8 = 3   # E4M3 elements + E8M0 scales per 32 along K, bf16 output
+FP32 = 4    # activations, weights and gradients of layer_norm and the calls after it
 OK, EINVAL, EUNSUPPORTED, EHIP, ENOMEM = 0, -1, -2, -3, -4
 
 # every symbol the header declares
@@ -35,6 +38,8 @@ EXPORTS = (
     "tsgemm_mx_pack_scales", "tsgemm_run_mx_packed", "tsgemm_num_tiles", "tsgemm_num_workgroups", "tsgemm_plan_info",
     "tsgemm_dump_schedule", "tsgemm_schedule_host", "tsgemm_destroy", "tsgemm_last_error",
     "tsgemm_last_error_code", "tsgemm_launch_info", "tsgemm_run_mx_noalloc", "tsgemm_worker_numbering",
+    "tsgemm_layer_norm", "tsgemm_layer_norm_grad_workspace", "tsgemm_layer_norm_grad", "tsgemm_mx_quantize",
+    "tsgemm_mx_dequantize", "tsgemm_mx_weight_grad_workspace", "tsgemm_mx_weight_grad",
 )
 
 
@@ -130,6 +135,21 @@ def load(path: str | None = None):
     lib.tsgemm_launch_info.restype = i32
     lib.tsgemm_worker_numbering.argtypes = [i32, i32, i32, i32p]
     lib.tsgemm_worker_numbering.restype = i32
+    f32 = ctypes.c_float
+    lib.tsgemm_layer_norm.argtypes = [i64, i64, i32, i32, vp, i64, vp, vp, f32, vp, i64, vp, vp, vp, vp, vp]
+    lib.tsgemm_layer_norm.restype = i32
+    lib.tsgemm_layer_norm_grad_workspace.argtypes = [i64, i64]
+    lib.tsgemm_layer_norm_grad_workspace.restype = i64
+    lib.tsgemm_layer_norm_grad.argtypes = [i64, i64, i32, i32, vp, i64, vp, i64, vp, vp, vp, vp, i64, vp, vp, vp, i64, vp]
+    lib.tsgemm_layer_norm_grad.restype = i32
+    lib.tsgemm_mx_quantize.argtypes = [i64, i64, i32, vp, i64, vp, vp, vp]
+    lib.tsgemm_mx_quantize.restype = i32
+    lib.tsgemm_mx_dequantize.argtypes = [i64, i64, i32, vp, vp, vp, i64, vp]
+    lib.tsgemm_mx_dequantize.restype = i32
+    lib.tsgemm_mx_weight_grad_workspace.argtypes = [i64, i64, i64]
+    lib.tsgemm_mx_weight_grad_workspace.restype = i64
+    lib.tsgemm_mx_weight_grad.argtypes = [i64, i64, i64, i32, i32, vp, i64, vp, vp, vp, vp, i64, vp]
+    lib.tsgemm_mx_weight_grad.restype = i32
     if path is None:
         _lib = lib
     return lib
@@ -330,6 +350,182 @@ class Plan:
         t = self._check_trace(trace)
         s = (stream or torch.cuda.current_stream(C.device)).cuda_stream
         _check(self._lib.tsgemm_run_mx_traced(self._h, a, sa, b, sb, c, s, t))
+
+
+# ---- what a normalised linear layer needs around the MXFP8 product -----------
+_FLOATS = None  # torch dtype -> code, filled on the first call (torch is imported late here)
+
+
+def _float_codes():
+    global _FLOATS
+    if _FLOATS is None:
+        import torch
+        _FLOATS = {torch.float16: FP16, torch.bfloat16: BF16, torch.float32: FP32}
+    return _FLOATS
+
+
+def _matrix(name, t, rows, width, like=None):
+    """Device pointer and row stride of a [rows, width] floating-point tensor."""
+    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != width or not t.is_cuda \
+            or (like is not None and (t.dtype != like.dtype or t.device != like.device)):
+        raise ValueError(f"{name} must be a CUDA tensor of shape {(rows, width)}"
+                         + (f", {like.dtype}, on {like.device}" if like is not None else ""))
+    ld, one = t.stride()
+    if rows <= 1:
+        ld = max(width, 1)
+    if (one != 1 and width > 1) or ld < width:
+        raise ValueError(f"{name} must have contiguous rows")
+    return t.data_ptr(), ld
+
+
+def _vector(name, t, n, dtype, like):
+    if t.dtype != dtype or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous() or t.device != like.device:
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {(n,)} on {like.device}")
+    return t.data_ptr()
+
+
+def _mx(codes, scales, rows, width, like):
+    import torch
+    if width % 32:
+        raise ValueError(f"MX blocks need a width divisible by 32, got {width}")
+    for name, t, shape in (("codes", codes, (rows, width)), ("scales", scales, (rows, width // 32))):
+        if t is None or t.element_size() != 1 or t.dtype == torch.bool or t.shape != shape or not t.is_contiguous() \
+                or t.device != like.device:
+            raise ValueError(f"{name} must be a contiguous 1-byte tensor of shape {shape} on {like.device}")
+    return codes.data_ptr(), scales.data_ptr()
+
+
+def _dtype_code(name, t):
+    code = _float_codes().get(t.dtype)
+    if code is None:
+        raise ValueError(f"{name} must be float16, bfloat16 or float32, got {t.dtype}")
+    return code
+
+
+def _stream_of(t, stream):
+    import torch
+    return (stream or torch.cuda.current_stream(t.device)).cuda_stream
+
+
+def _workspace(nbytes, workspace, like, stream):
+    """Pointer and tensor of a workspace: the caller's, or one of torch's
+    allocator, taken for the stream that the kernels run on."""
+    import torch
+    if workspace is not None:
+        if workspace.device != like.device or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be a contiguous tensor on {like.device}")
+        return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+    if nbytes == 0:
+        return None, 0, None
+    if stream is None:
+        t = torch.empty(nbytes, dtype=torch.uint8, device=like.device)
+    else:
+        with torch.cuda.stream(stream):
+            t = torch.empty(nbytes, dtype=torch.uint8, device=like.device)
+    return t.data_ptr(), nbytes, t
+
+
+def layer_norm(x, gamma, beta, eps, y=None, mean=None, rstd=None, codes=None, scales=None, stream=None) -> None:
+    """tsgemm_layer_norm: y = (x - mean) * rstd * gamma + beta for every row of
+    x[rows, width], written to `y` (x's dtype), or as MX to `codes` and `scales`
+    (the A and SFA of run_mx; any 1-byte dtype), or both.  gamma and beta (None:
+    ones, zeros) are of x's dtype or float32; mean and rstd, float32[rows], are
+    given together or not at all."""
+    import torch
+    if x.dim() != 2:
+        raise ValueError("x must have two dimensions")
+    rows, width = x.shape
+    dt = _dtype_code("x", x)
+    px, ldx = _matrix("x", x, rows, width)
+    w = gamma if gamma is not None else beta
+    wdtype = x.dtype if w is None else w.dtype
+    wdt = dt if w is None else _dtype_code("gamma and beta", w)
+    pg = None if gamma is None else _vector("gamma", gamma, width, wdtype, x)
+    pb = None if beta is None else _vector("beta", beta, width, wdtype, x)
+    py, ldy = (None, 0) if y is None else _matrix("y", y, rows, width, x)
+    pm = None if mean is None else _vector("mean", mean, rows, torch.float32, x)
+    pr = None if rstd is None else _vector("rstd", rstd, rows, torch.float32, x)
+    pc, ps = (None, None) if codes is None and scales is None else _mx(codes, scales, rows, width, x)
+    _check(load().tsgemm_layer_norm(rows, width, dt, wdt, px, ldx, pg, pb, eps, py, ldy, pm, pr, pc, ps,
+                                    _stream_of(x, stream)))
+
+
+def layer_norm_grad(dy, x, gamma, mean, rstd, dx, dgamma=None, dbeta=None, workspace=None, stream=None) -> None:
+    """tsgemm_layer_norm_grad: dx[rows, width], dgamma[width] and dbeta[width]
+    (None: not wanted) from dy, x and what layer_norm left in mean and rstd.  dy
+    and dx are of x's dtype; gamma (None: ones), dgamma and dbeta share one, x's
+    or float32.  `workspace`: a tensor to keep the workgroups' sums in
+    (layer_norm_grad_workspace bytes); by default torch's allocator gives one."""
+    import torch
+    if x.dim() != 2:
+        raise ValueError("x must have two dimensions")
+    rows, width = x.shape
+    dt = _dtype_code("x", x)
+    px, ldx = _matrix("x", x, rows, width)
+    pdy, lddy = _matrix("dy", dy, rows, width, x)
+    pdx, lddx = _matrix("dx", dx, rows, width, x)
+    w = gamma if gamma is not None else dgamma if dgamma is not None else dbeta
+    wdtype = x.dtype if w is None else w.dtype
+    wdt = dt if w is None else _dtype_code("gamma, dgamma and dbeta", w)
+    pg = None if gamma is None else _vector("gamma", gamma, width, wdtype, x)
+    pdg = None if dgamma is None else _vector("dgamma", dgamma, width, wdtype, x)
+    pdb = None if dbeta is None else _vector("dbeta", dbeta, width, wdtype, x)
+    pm = _vector("mean", mean, rows, torch.float32, x)
+    pr = _vector("rstd", rstd, rows, torch.float32, x)
+    need = 0 if pdg is None and pdb is None else layer_norm_grad_workspace(rows, width)
+    pw, have, keep = _workspace(need, workspace, x, stream)
+    _check(load().tsgemm_layer_norm_grad(rows, width, dt, wdt, pdy, lddy, px, ldx, pg, pm, pr, pdx, lddx, pdg, pdb,
+                                         pw, have, _stream_of(x, stream)))
+
+
+def layer_norm_grad_workspace(rows: int, width: int) -> int:
+    """Bytes of workspace a layer_norm_grad of this shape takes."""
+    return _check(load().tsgemm_layer_norm_grad_workspace(rows, width))
+
+
+def mx_quantize(x, codes, scales, stream=None) -> None:
+    """tsgemm_mx_quantize: x[rows, width] -> E4M3 codes[rows, width] and E8M0
+    scales[rows, width / 32] (any 1-byte dtype), the operands of run_mx."""
+    if x.dim() != 2:
+        raise ValueError("x must have two dimensions")
+    rows, width = x.shape
+    px, ldx = _matrix("x", x, rows, width)
+    pc, ps = _mx(codes, scales, rows, width, x)
+    _check(load().tsgemm_mx_quantize(rows, width, _dtype_code("x", x), px, ldx, pc, ps, _stream_of(x, stream)))
+
+
+def mx_dequantize(codes, scales, out, stream=None) -> None:
+    """tsgemm_mx_dequantize: out[rows, width] = code * scale, rounded once to out's dtype."""
+    if out.dim() != 2:
+        raise ValueError("out must have two dimensions")
+    rows, width = out.shape
+    po, ldo = _matrix("out", out, rows, width)
+    pc, ps = _mx(codes, scales, rows, width, out)
+    _check(load().tsgemm_mx_dequantize(rows, width, _dtype_code("out", out), pc, ps, po, ldo, _stream_of(out, stream)))
+
+
+def mx_weight_grad(dy, codes, scales, dw, workspace=None, stream=None) -> None:
+    """tsgemm_mx_weight_grad: dw[out, width] = dy[rows, out]^T times the MX
+    activation (codes, scales).  dy is float16 or bfloat16, dw of dy's dtype or
+    float32.  `workspace`: a tensor for the split rows' products
+    (mx_weight_grad_workspace bytes); by default torch's allocator gives one."""
+    if dy.dim() != 2 or dw.dim() != 2:
+        raise ValueError("dy and dw must have two dimensions")
+    rows, out = dy.shape
+    width = dw.shape[1]
+    pdy, lddy = _matrix("dy", dy, rows, out)
+    dt, gdt = _dtype_code("dy", dy), _dtype_code("dw", dw)
+    if tuple(dw.shape) != (out, width) or not dw.is_contiguous() or dw.device != dy.device:
+        raise ValueError(f"dw must be a contiguous tensor of shape {(out, width)} on {dy.device}")
+    pc, ps = _mx(codes, scales, rows, width, dy)
+    pw, have, keep = _workspace(mx_weight_grad_workspace(rows, out, width), workspace, dy, stream)
+    _check(load().tsgemm_mx_weight_grad(rows, out, width, dt, gdt, pdy, lddy, pc, ps, dw.data_ptr(), pw, have,
+                                        _stream_of(dy, stream)))
+
+
+def mx_weight_grad_workspace(rows: int, out: int, width: int) -> int:
+    """Bytes of workspace an mx_weight_grad of this shape takes (0: none)."""
+    return _check(load().tsgemm_mx_weight_grad_workspace(rows, out, width))
 
 
 def worker_numbering(num_workgroups: int, num_xcds: int, num_active: int) -> np.ndarray:

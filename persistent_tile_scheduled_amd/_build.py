@@ -2,8 +2,10 @@
 
 The kernels are split over translation units that compile in parallel: the
 host code (tsgemm.hip), one unit per fp16/bf16 dtype and tile shape
-(tsgemm_gemm_tu.hip with -DTSG_TU_*), and the block-scaled FP8 unit
-(tsgemm_mx_tu.hip).  The objects are linked into one shared library.
+(tsgemm_gemm_tu.hip with -DTSG_TU_*), the block-scaled FP8 unit
+(tsgemm_mx_tu.hip), and the operators around it: their host code
+(tsgemm_ops.hip), the row operators (tsgemm_rows_tu.hip) and the weight
+gradient (tsgemm_wgrad_tu.hip).  The objects are linked into one shared library.
 """
 
 from __future__ import annotations
@@ -29,7 +31,9 @@ FLAGS = [
 
 # (source, extra defines, object name)
 GEMM_TUS = [(dt, bm, bk) for dt in (1, 2) for bm in (128, 256) for bk in (32, 64)]
-UNITS = ([("tsgemm.hip", [], "host.o"), ("tsgemm_mx_tu.hip", [], "mx.o")] +
+UNITS = ([("tsgemm.hip", [], "host.o"), ("tsgemm_mx_tu.hip", [], "mx.o"),
+          ("tsgemm_ops.hip", [], "ops.o"), ("tsgemm_rows_tu.hip", [], "rows.o"),
+          ("tsgemm_wgrad_tu.hip", [], "wgrad.o")] +
          [("tsgemm_gemm_tu.hip", [f"-DTSG_TU_DT={dt}", f"-DTSG_TU_BM={bm}", f"-DTSG_TU_BK={bk}"],
            f"gemm_{dt}_{bm}_{bk}.o") for dt, bm, bk in GEMM_TUS])
 
