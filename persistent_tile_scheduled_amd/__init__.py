@@ -353,70 +353,97 @@ class Plan:
 
 
 # ---- what a normalised linear layer needs around the MXFP8 product -----------
-_FLOATS = None  # torch dtype -> code, filled on the first call (torch is imported late here)
+# At the smallest shapes a call costs what the host spends on it, so the checks
+# below ask each tensor for each property once and build no message they do not
+# raise.
+_FLOATS = {}         # torch dtype -> code, filled on the first call (torch is imported late here)
+_BOOL = None         # torch.bool
+_raw_stream = None   # device index -> handle of torch's current stream
 
 
-def _float_codes():
-    global _FLOATS
-    if _FLOATS is None:
-        import torch
-        _FLOATS = {torch.float16: FP16, torch.bfloat16: BF16, torch.float32: FP32}
-    return _FLOATS
-
-
-def _matrix(name, t, rows, width, like=None):
-    """Device pointer and row stride of a [rows, width] floating-point tensor."""
-    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != width or not t.is_cuda \
-            or (like is not None and (t.dtype != like.dtype or t.device != like.device)):
-        raise ValueError(f"{name} must be a CUDA tensor of shape {(rows, width)}"
-                         + (f", {like.dtype}, on {like.device}" if like is not None else ""))
-    ld, one = t.stride()
-    if rows <= 1:
-        ld = max(width, 1)
-    if (one != 1 and width > 1) or ld < width:
-        raise ValueError(f"{name} must have contiguous rows")
-    return t.data_ptr(), ld
-
-
-def _vector(name, t, n, dtype, like):
-    if t.dtype != dtype or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous() or t.device != like.device:
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {(n,)} on {like.device}")
-    return t.data_ptr()
-
-
-def _mx(codes, scales, rows, width, like):
+def _first_call():
+    global _BOOL, _raw_stream
     import torch
-    if width % 32:
-        raise ValueError(f"MX blocks need a width divisible by 32, got {width}")
-    for name, t, shape in (("codes", codes, (rows, width)), ("scales", scales, (rows, width // 32))):
-        if t is None or t.element_size() != 1 or t.dtype == torch.bool or t.shape != shape or not t.is_contiguous() \
-                or t.device != like.device:
-            raise ValueError(f"{name} must be a contiguous 1-byte tensor of shape {shape} on {like.device}")
-    return codes.data_ptr(), scales.data_ptr()
+    _BOOL = torch.bool
+    _FLOATS.update({torch.float16: FP16, torch.bfloat16: BF16, torch.float32: FP32})
+    # the same handle as torch.cuda.current_stream(device).cuda_stream without
+    # the Stream object around it (0.1 us instead of 1.8)
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+        (lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
-def _dtype_code(name, t):
-    code = _float_codes().get(t.dtype)
+def _dtype_code(name, dtype):
+    if not _FLOATS:
+        _first_call()
+    code = _FLOATS.get(dtype)
     if code is None:
-        raise ValueError(f"{name} must be float16, bfloat16 or float32, got {t.dtype}")
+        raise ValueError(f"{name} must be float16, bfloat16 or float32, got {dtype}")
     return code
 
 
-def _stream_of(t, stream):
-    import torch
-    return (stream or torch.cuda.current_stream(t.device)).cuda_stream
+def _rows_width(name, t):
+    """Rows, width, device index and row stride of a two-dimensional GPU tensor with contiguous rows."""
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError(f"{name} must have two dimensions")
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return shape[0], shape[1], dev, _row_stride(name, t, shape[0], shape[1])
+
+
+def _row_stride(name, t, rows, width):
+    ld, one = t.stride()
+    if rows <= 1:
+        ld = width
+    if (one != 1 and width > 1) or ld < width:
+        raise ValueError(f"{name} must have contiguous rows")
+    return ld
+
+
+def _matrix(name, t, shape, dtype, dev):
+    """Pointer and row stride of another matrix of the call."""
+    if t.shape != shape or t.dtype != dtype or t.get_device() != dev:
+        raise ValueError(f"{name} must be a {dtype} tensor of shape {tuple(shape)} on CUDA device {dev}")
+    return t.data_ptr(), _row_stride(name, t, shape[0], shape[1])
+
+
+def _vector(name, t, n, dtype, dev):
+    if t is None:
+        return None
+    if t.dtype != dtype or t.shape != (n,) or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {(n,)} on CUDA device {dev}")
+    return t.data_ptr()
+
+
+def _mx(codes, scales, rows, width, dev):
+    if width % 32:
+        raise ValueError(f"MX blocks need a width divisible by 32, got {width}")
+    if codes is None or scales is None:
+        raise ValueError("codes and scales are given together")
+    if codes.shape != (rows, width) or codes.element_size() != 1 or codes.dtype is _BOOL or codes.get_device() != dev \
+            or not codes.is_contiguous():
+        raise ValueError(f"codes must be a contiguous 1-byte tensor of shape {(rows, width)} on CUDA device {dev}")
+    if scales.shape != (rows, width // 32) or scales.element_size() != 1 or scales.dtype is _BOOL or scales.get_device() != dev \
+            or not scales.is_contiguous():
+        raise ValueError(f"scales must be a contiguous 1-byte tensor of shape {(rows, width // 32)} on CUDA device {dev}")
+    return codes.data_ptr(), scales.data_ptr()
+
+
+def _stream_of(dev, stream):
+    return _raw_stream(dev) if stream is None else stream.cuda_stream
 
 
 def _workspace(nbytes, workspace, like, stream):
-    """Pointer and tensor of a workspace: the caller's, or one of torch's
+    """Pointer, size and tensor of a workspace: the caller's, or one of torch's
     allocator, taken for the stream that the kernels run on."""
-    import torch
     if workspace is not None:
         if workspace.device != like.device or not workspace.is_contiguous():
             raise ValueError(f"workspace must be a contiguous tensor on {like.device}")
         return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
     if nbytes == 0:
         return None, 0, None
+    import torch
     if stream is None:
         t = torch.empty(nbytes, dtype=torch.uint8, device=like.device)
     else:
@@ -431,23 +458,24 @@ def layer_norm(x, gamma, beta, eps, y=None, mean=None, rstd=None, codes=None, sc
     (the A and SFA of run_mx; any 1-byte dtype), or both.  gamma and beta (None:
     ones, zeros) are of x's dtype or float32; mean and rstd, float32[rows], are
     given together or not at all."""
-    import torch
-    if x.dim() != 2:
-        raise ValueError("x must have two dimensions")
-    rows, width = x.shape
-    dt = _dtype_code("x", x)
-    px, ldx = _matrix("x", x, rows, width)
+    xdt = x.dtype
+    dt = _dtype_code("x", xdt)
+    rows, width, dev, ldx = _rows_width("x", x)
     w = gamma if gamma is not None else beta
-    wdtype = x.dtype if w is None else w.dtype
-    wdt = dt if w is None else _dtype_code("gamma and beta", w)
-    pg = None if gamma is None else _vector("gamma", gamma, width, wdtype, x)
-    pb = None if beta is None else _vector("beta", beta, width, wdtype, x)
-    py, ldy = (None, 0) if y is None else _matrix("y", y, rows, width, x)
-    pm = None if mean is None else _vector("mean", mean, rows, torch.float32, x)
-    pr = None if rstd is None else _vector("rstd", rstd, rows, torch.float32, x)
-    pc, ps = (None, None) if codes is None and scales is None else _mx(codes, scales, rows, width, x)
-    _check(load().tsgemm_layer_norm(rows, width, dt, wdt, px, ldx, pg, pb, eps, py, ldy, pm, pr, pc, ps,
-                                    _stream_of(x, stream)))
+    wtype = xdt if w is None else w.dtype
+    wdt = dt if wtype is xdt else _dtype_code("gamma and beta", wtype)
+    pg = _vector("gamma", gamma, width, wtype, dev)
+    pb = _vector("beta", beta, width, wtype, dev)
+    py, ldy = (None, 0) if y is None else _matrix("y", y, x.shape, xdt, dev)
+    pm = pr = pc = ps = None
+    if mean is not None or rstd is not None:
+        import torch
+        pm = _vector("mean", mean, rows, torch.float32, dev)
+        pr = _vector("rstd", rstd, rows, torch.float32, dev)
+    if codes is not None or scales is not None:
+        pc, ps = _mx(codes, scales, rows, width, dev)
+    _check(load().tsgemm_layer_norm(rows, width, dt, wdt, x.data_ptr(), ldx, pg, pb, eps, py, ldy, pm, pr, pc, ps,
+                                    _stream_of(dev, stream)))
 
 
 def layer_norm_grad(dy, x, gamma, mean, rstd, dx, dgamma=None, dbeta=None, workspace=None, stream=None) -> None:
@@ -457,25 +485,25 @@ def layer_norm_grad(dy, x, gamma, mean, rstd, dx, dgamma=None, dbeta=None, works
     or float32.  `workspace`: a tensor to keep the workgroups' sums in
     (layer_norm_grad_workspace bytes); by default torch's allocator gives one."""
     import torch
-    if x.dim() != 2:
-        raise ValueError("x must have two dimensions")
-    rows, width = x.shape
-    dt = _dtype_code("x", x)
-    px, ldx = _matrix("x", x, rows, width)
-    pdy, lddy = _matrix("dy", dy, rows, width, x)
-    pdx, lddx = _matrix("dx", dx, rows, width, x)
+    xdt, f32 = x.dtype, torch.float32
+    dt = _dtype_code("x", xdt)
+    rows, width, dev, ldx = _rows_width("x", x)
+    pdy, lddy = _matrix("dy", dy, x.shape, xdt, dev)
+    pdx, lddx = _matrix("dx", dx, x.shape, xdt, dev)
     w = gamma if gamma is not None else dgamma if dgamma is not None else dbeta
-    wdtype = x.dtype if w is None else w.dtype
-    wdt = dt if w is None else _dtype_code("gamma, dgamma and dbeta", w)
-    pg = None if gamma is None else _vector("gamma", gamma, width, wdtype, x)
-    pdg = None if dgamma is None else _vector("dgamma", dgamma, width, wdtype, x)
-    pdb = None if dbeta is None else _vector("dbeta", dbeta, width, wdtype, x)
-    pm = _vector("mean", mean, rows, torch.float32, x)
-    pr = _vector("rstd", rstd, rows, torch.float32, x)
+    wtype = xdt if w is None else w.dtype
+    wdt = dt if wtype is xdt else _dtype_code("gamma, dgamma and dbeta", wtype)
+    pg = _vector("gamma", gamma, width, wtype, dev)
+    pdg = _vector("dgamma", dgamma, width, wtype, dev)
+    pdb = _vector("dbeta", dbeta, width, wtype, dev)
+    if mean is None or rstd is None:
+        raise ValueError("mean and rstd must be given")
+    pm = _vector("mean", mean, rows, f32, dev)
+    pr = _vector("rstd", rstd, rows, f32, dev)
     need = 0 if pdg is None and pdb is None else layer_norm_grad_workspace(rows, width)
     pw, have, keep = _workspace(need, workspace, x, stream)
-    _check(load().tsgemm_layer_norm_grad(rows, width, dt, wdt, pdy, lddy, px, ldx, pg, pm, pr, pdx, lddx, pdg, pdb,
-                                         pw, have, _stream_of(x, stream)))
+    _check(load().tsgemm_layer_norm_grad(rows, width, dt, wdt, pdy, lddy, x.data_ptr(), ldx, pg, pm, pr, pdx, lddx, pdg,
+                                         pdb, pw, have, _stream_of(dev, stream)))
 
 
 def layer_norm_grad_workspace(rows: int, width: int) -> int:
@@ -486,22 +514,18 @@ def layer_norm_grad_workspace(rows: int, width: int) -> int:
 def mx_quantize(x, codes, scales, stream=None) -> None:
     """tsgemm_mx_quantize: x[rows, width] -> E4M3 codes[rows, width] and E8M0
     scales[rows, width / 32] (any 1-byte dtype), the operands of run_mx."""
-    if x.dim() != 2:
-        raise ValueError("x must have two dimensions")
-    rows, width = x.shape
-    px, ldx = _matrix("x", x, rows, width)
-    pc, ps = _mx(codes, scales, rows, width, x)
-    _check(load().tsgemm_mx_quantize(rows, width, _dtype_code("x", x), px, ldx, pc, ps, _stream_of(x, stream)))
+    dt = _dtype_code("x", x.dtype)
+    rows, width, dev, ldx = _rows_width("x", x)
+    pc, ps = _mx(codes, scales, rows, width, dev)
+    _check(load().tsgemm_mx_quantize(rows, width, dt, x.data_ptr(), ldx, pc, ps, _stream_of(dev, stream)))
 
 
 def mx_dequantize(codes, scales, out, stream=None) -> None:
     """tsgemm_mx_dequantize: out[rows, width] = code * scale, rounded once to out's dtype."""
-    if out.dim() != 2:
-        raise ValueError("out must have two dimensions")
-    rows, width = out.shape
-    po, ldo = _matrix("out", out, rows, width)
-    pc, ps = _mx(codes, scales, rows, width, out)
-    _check(load().tsgemm_mx_dequantize(rows, width, _dtype_code("out", out), pc, ps, po, ldo, _stream_of(out, stream)))
+    dt = _dtype_code("out", out.dtype)
+    rows, width, dev, ldo = _rows_width("out", out)
+    pc, ps = _mx(codes, scales, rows, width, dev)
+    _check(load().tsgemm_mx_dequantize(rows, width, dt, pc, ps, out.data_ptr(), ldo, _stream_of(dev, stream)))
 
 
 def mx_weight_grad(dy, codes, scales, dw, workspace=None, stream=None) -> None:
@@ -509,18 +533,15 @@ def mx_weight_grad(dy, codes, scales, dw, workspace=None, stream=None) -> None:
     activation (codes, scales).  dy is float16 or bfloat16, dw of dy's dtype or
     float32.  `workspace`: a tensor for the split rows' products
     (mx_weight_grad_workspace bytes); by default torch's allocator gives one."""
-    if dy.dim() != 2 or dw.dim() != 2:
-        raise ValueError("dy and dw must have two dimensions")
-    rows, out = dy.shape
-    width = dw.shape[1]
-    pdy, lddy = _matrix("dy", dy, rows, out)
-    dt, gdt = _dtype_code("dy", dy), _dtype_code("dw", dw)
-    if tuple(dw.shape) != (out, width) or not dw.is_contiguous() or dw.device != dy.device:
-        raise ValueError(f"dw must be a contiguous tensor of shape {(out, width)} on {dy.device}")
-    pc, ps = _mx(codes, scales, rows, width, dy)
+    dt, gdt = _dtype_code("dy", dy.dtype), _dtype_code("dw", dw.dtype)
+    rows, out, dev, lddy = _rows_width("dy", dy)
+    width = dw.shape[-1]
+    if dw.shape != (out, width) or dw.get_device() != dev or not dw.is_contiguous():
+        raise ValueError(f"dw must be a contiguous tensor of shape {(out, width)} on CUDA device {dev}")
+    pc, ps = _mx(codes, scales, rows, width, dev)
     pw, have, keep = _workspace(mx_weight_grad_workspace(rows, out, width), workspace, dy, stream)
-    _check(load().tsgemm_mx_weight_grad(rows, out, width, dt, gdt, pdy, lddy, pc, ps, dw.data_ptr(), pw, have,
-                                        _stream_of(dy, stream)))
+    _check(load().tsgemm_mx_weight_grad(rows, out, width, dt, gdt, dy.data_ptr(), lddy, pc, ps, dw.data_ptr(), pw, have,
+                                        _stream_of(dev, stream)))
 
 
 def mx_weight_grad_workspace(rows: int, out: int, width: int) -> int:

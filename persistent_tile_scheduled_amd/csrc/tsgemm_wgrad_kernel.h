@@ -5,8 +5,16 @@
 // dy is fp16 or bf16, x() an E4M3 element, s() an E8M0 scale (OCP Microscaling
 // Formats specification v1.0).  The sum runs over the rows, across which the
 // scales change, so the block-scaled matrix instruction (one scale per 32 terms
-// of the sum) cannot take them: the codes are decoded on their way into LDS, to
-// bf16, which holds every element times scale of the fp32 range exactly.
+// of the sum) cannot take them: the codes are decoded on their way into LDS.
+//   * bf16 dy: to bf16, which holds every element times scale of the fp32 range
+//     exactly.
+//   * fp16 dy: to fp16, times 2^kShift, which dw is divided by in the end.  That
+//     is exact for scales of 2^kScaleLow ... 2^kScaleHigh: the least element
+//     2^-9 becomes at least fp16's least 2^-24, the largest 448 at most 57344.
+//     Blocks of activations whose largest magnitude is between 2^-13 and 2^10
+//     have such scales.  A 64-row slab with a block outside (other than one of
+//     zeros) is multiplied in bf16 instead, with dy split into two bf16 values
+//     whose sum it is, at half the rate: no term loses a bit either way.
 //
 // Both operands lie with the sum's index slowest, [row][column], and both come
 // out of LDS through the transpose read ds_read_b64_tr_b16.  One workgroup of
@@ -54,20 +62,26 @@ struct WgradTraits {
     static_assert(NP >= 1 && LDS <= 160 * 1024, "tile");
 };
 
+// How a slab is multiplied: bf16 dy; fp16 dy with codes as fp16; fp16 dy split.
+enum { WG_BF16 = 0, WG_FP16 = 1, WG_SPLIT = 2 };
+constexpr int kShift = 6, kScaleLow = -15 - kShift, kScaleHigh = 7 - kShift;
+constexpr uint32_t kSplitSlabs = 16;  // slabs multiplied in bf16 before fp16 is tried again
+
 // acc += a * b as mfma16x16x32, for operands that vector instructions have just
 // written: the two wait states cover what the compiler would place.
 __device__ __forceinline__ void mfma_bf16_settled(f32x4& acc, i16x8 a, i16x8 b) {
     asm volatile("s_nop 1\n\tv_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(acc) : "v"(a), "v"(b));
 }
 
-// 8 fp16 values = hi + lo in bf16, exactly (11 significant bits in 8 + 3).
+// 8 fp16 values times 2^kShift = hi + lo in bf16, exactly (11 significant bits in 8 + 3).
 __device__ __forceinline__ void split_f16(i16x8 v, i16x8& hi, i16x8& lo) {
     const f16x8 x = __builtin_bit_cast(f16x8, v);
     bf16x8 h, l;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-        h[e] = (__bf16)(float)x[e];
-        l[e] = (__bf16)((float)x[e] - (float)h[e]);
+        const float f = (float)x[e] * (float)(1 << kShift);
+        h[e] = (__bf16)f;
+        l[e] = (__bf16)(f - (float)h[e]);
     }
     hi = __builtin_bit_cast(i16x8, h);
     lo = __builtin_bit_cast(i16x8, l);
@@ -78,6 +92,7 @@ __global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void wgrad_kernel(WgradArgs
     using T = WgradTraits<BM, BN>;
     constexpr int FM = T::FM, FN = T::FN, NA = T::NA, NP = T::NP;
     __shared__ __attribute__((aligned(1024))) uint8_t smem[T::LDS];
+    __shared__ __attribute__((aligned(16))) uint32_t flags[2][4];  // fp16: a slab needs the split, by wave
     typedef __attribute__((address_space(3))) uint8_t lds_u8;
     typedef __attribute__((address_space(3))) u32x4 lds_u32x4;
     const uint32_t lds_base = (uint32_t)reinterpret_cast<uintptr_t>((lds_u8*)smem);
@@ -105,13 +120,16 @@ __global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void wgrad_kernel(WgradArgs
     // past the end read zeros; columns past the end read the next row's values,
     // which only reach columns of dw that are not stored.
     const uint32_t a_pitch = (uint32_t)args.lddy * 2u;
-    uint64_t a_ptr = reinterpret_cast<uint64_t>(args.dy) + (uint64_t)slab0 * T::BK * a_pitch + (uint64_t)m0 * 2u;
-    uint64_t c_ptr = reinterpret_cast<uint64_t>(args.codes) + (uint64_t)slab0 * T::BK * width + n0;
-    uint64_t s_ptr = reinterpret_cast<uint64_t>(args.scales) + (uint64_t)slab0 * T::BK * w32 + n0 / 32u;
-    const int64_t rows_here = args.rows - (int64_t)slab0 * T::BK;
-    const int64_t rows_split = (int64_t)slabs * T::BK;
-    int64_t left = rows_here < rows_split ? rows_here : rows_split;
-    int32_t a_left = left < 0 ? 0 : left > (int64_t)0x7FFFFFFF ? 0x7FFFFFFF : (int32_t)left, c_left = a_left;
+    uint64_t a_ptr = 0, c_ptr = 0, s_ptr = 0;
+    int32_t a_left = 0, c_left = 0;
+    auto seek = [&](uint32_t slab) __attribute__((always_inline)) {  // of this workgroup's
+        const int64_t r0 = (int64_t)(slab0 + slab) * T::BK;
+        a_ptr = reinterpret_cast<uint64_t>(args.dy) + (uint64_t)r0 * a_pitch + (uint64_t)m0 * 2u;
+        c_ptr = reinterpret_cast<uint64_t>(args.codes) + (uint64_t)r0 * width + n0;
+        s_ptr = reinterpret_cast<uint64_t>(args.scales) + (uint64_t)r0 * w32 + n0 / 32u;
+        const int64_t all = args.rows - r0, here = (int64_t)(slabs - slab) * T::BK;
+        a_left = c_left = (int32_t)(all < here ? all : here);  // rows < 2^31
+    };
     auto span = [](int32_t l, uint32_t pitch, uint32_t last) __attribute__((always_inline)) -> uint32_t {
         const uint32_t r = l <= 0 ? 0u : l < T::BK ? (uint32_t)l : (uint32_t)T::BK;
         return r == 0u ? 0u : (r - 1u) * pitch + last;
@@ -170,16 +188,51 @@ __global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void wgrad_kernel(WgradArgs
     uint32_t b_wr[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) b_wr[j] = lds_base + T::B_OFF + kr * T::B_ROW + ((nb * 4u + j) ^ swz_b(kr)) * 16u;
-    auto convert = [&](auto r_c, auto s_c, auto i_c) __attribute__((always_inline)) {  // raw set, stage, op i of 4 * NP
-        constexpr int R = decltype(r_c)::value, S = decltype(s_c)::value, p = decltype(i_c)::value / 4, j = decltype(i_c)::value % 4;
-        const float s = __builtin_bit_cast(float, scl[R][p] << 23);
+    auto convert = [&](auto mode_c, auto s_c, auto i_c) __attribute__((always_inline)) {  // stage and raw set, op i of 4 * NP
+        constexpr int MODE = decltype(mode_c)::value, S = decltype(s_c)::value, R = S;
+        constexpr int p = decltype(i_c)::value / 4, j = decltype(i_c)::value % 4;
+        uint32_t field = scl[R][p];
+        if constexpr (MODE == WG_FP16) field = field + kShift < 255u ? field + kShift : 255u;  // 255, a NaN, stays one
+        const float s = __builtin_bit_cast(float, field << 23);
         const uint32_t w0 = raw[R][p][j / 2][2 * (j % 2)], w1 = raw[R][p][j / 2][2 * (j % 2) + 1];
         u32x4 v;
-        v.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w0, s, false));
-        v.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w0, s, true));
-        v.z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w1, s, false));
-        v.w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w1, s, true));
+        if constexpr (MODE == WG_FP16) {
+            v.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w0, s, false));
+            v.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w0, s, true));
+            v.z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w1, s, false));
+            v.w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w1, s, true));
+        } else {
+            v.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w0, s, false));
+            v.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w0, s, true));
+            v.z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w1, s, false));
+            v.w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w1, s, true));
+        }
         *(lds_u32x4*)((lds_u8*)(uintptr_t)b_wr[j] + S * T::B_STAGE + p * 32 * T::B_ROW) = v;
+    };
+
+    // fp16: does one of this thread's blocks in raw set S need the split?  A wave's
+    // answer goes to its word of flag row S; the workgroup's is read after the
+    // next barrier.
+    auto far_block = [&](auto s_c) __attribute__((always_inline)) -> bool {
+        constexpr int S = decltype(s_c)::value;
+        bool far = false;
+#pragma unroll
+        for (int p = 0; p < NP; ++p) {
+            uint32_t any = 0;
+#pragma unroll
+            for (int w = 0; w < 8; ++w) any |= raw[S][p][w / 4][w % 4];
+            const bool zeros = (any & 0x7F7F7F7Fu) == 0u && scl[S][p] + kShift < 255u;
+            far |= scl[S][p] - (uint32_t)(127 + kScaleLow) > (uint32_t)(kScaleHigh - kScaleLow) && !zeros && scl[S][p] != 255u;
+        }
+        return far;
+    };
+    auto put_flag = [&](auto s_c) __attribute__((always_inline)) {
+        const bool far = __builtin_amdgcn_ballot_w64(far_block(s_c)) != 0u;
+        if (lane == 0u) flags[decltype(s_c)::value][wave] = far ? 1u : 0u;
+    };
+    auto get_flag = [&](auto s_c) __attribute__((always_inline)) -> bool {
+        const u32x4 f = *(const u32x4*)flags[decltype(s_c)::value];
+        return __builtin_amdgcn_readfirstlane(f.x | f.y | f.z | f.w) != 0u;
     };
 
     // ---- fragments.  As in the fp16/bf16 GEMM's B operand: the columns of a
@@ -228,18 +281,18 @@ __global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void wgrad_kernel(WgradArgs
     // One 32-row k-step on set K: FM * FN MFMAs, rows of blocks in order, the
     // columns there and back.  `between(s)` issues what goes after MFMA s.
     i16x8 hi, lo;
-    auto kstep = [&](auto k_c, auto&& between) __attribute__((always_inline)) {
-        constexpr int K = decltype(k_c)::value;
+    auto kstep = [&](auto mode_c, auto k_c, auto&& between) __attribute__((always_inline)) {
+        constexpr int MODE = decltype(mode_c)::value, K = decltype(k_c)::value;
         static_for<0, FM * FN>([&](auto s_c) __attribute__((always_inline)) {
             constexpr int s = decltype(s_c)::value, fm = s / FN, fn = (fm & 1) ? FN - 1 - s % FN : s % FN;
             const i16x8 bv = __builtin_shufflevector(fb[K][fn][0], fb[K][fn][1], 0, 1, 2, 3, 4, 5, 6, 7);
             const i16x8 av = __builtin_shufflevector(fa[K][fm][0], fa[K][fm][1], 0, 1, 2, 3, 4, 5, 6, 7);
-            if constexpr (DT == DT_FP16) {
+            if constexpr (MODE == WG_SPLIT) {
                 if constexpr (s % FN == 0) split_f16(av, hi, lo);
                 mfma_bf16_settled(acc[fm][fn], bv, hi);
                 mfma_bf16_settled(acc[fm][fn], bv, lo);
             } else {
-                mfma16x16x32<DT_BF16>(acc[fm][fn], bv, av);
+                mfma16x16x32<MODE == WG_FP16 ? DT_FP16 : DT_BF16>(acc[fm][fn], bv, av);
             }
             between(s_c);
             __builtin_amdgcn_sched_barrier(0);
@@ -263,7 +316,7 @@ __global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void wgrad_kernel(WgradArgs
     // (the slab's) is refilled with the slab after next while the fragments come
     // from stage 1 - S.
     constexpr int LOADS = NA + 3 * NP;                 // DMAs, then loads of codes and scales
-    auto fill = [&](auto s_c, auto gap_c) __attribute__((always_inline)) {
+    auto fill = [&](auto mode_c, auto s_c, auto gap_c) __attribute__((always_inline)) {
         constexpr int S = decltype(s_c)::value;
         spread(std::integral_constant<int, LOADS>{}, std::integral_constant<int, GAPS / 2>{}, gap_c, [&](auto i_c) __attribute__((always_inline)) {
             constexpr int i = decltype(i_c)::value;
@@ -271,36 +324,46 @@ __global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void wgrad_kernel(WgradArgs
             else load_codes(std::integral_constant<int, 1 - S>{}, std::integral_constant<int, i - NA>{});
         });
         spread(std::integral_constant<int, 4 * NP>{}, std::integral_constant<int, GAPS - STEPS / 4>{}, gap_c,
-               [&](auto i_c) __attribute__((always_inline)) { convert(s_c, s_c, i_c); });
+               [&](auto i_c) __attribute__((always_inline)) { convert(mode_c, s_c, i_c); });
     };
-    auto period = [&](auto s_c) __attribute__((always_inline)) {
-        constexpr int S = decltype(s_c)::value;
+    // `end`: the slab that this pipeline stops before; brought forward when the
+    // codes of slab `next` (those that this period converts) need the split.
+    auto period = [&](auto mode_c, auto s_c, uint32_t next, uint32_t& end) __attribute__((always_inline)) {
+        constexpr int MODE = decltype(mode_c)::value, S = decltype(s_c)::value;
         using OTHER = std::integral_constant<int, 1 - S>;
         stress_pause<0>(wave, stress_ctr);
         wait_vm<0>();    // the next slab's dy and the codes after it have landed
+        if constexpr (MODE == WG_FP16) put_flag(s_c);
         lds_barrier();   // ... for every wave; stage S is read out, its successor written
         stress_pause<1>(wave, stress_ctr);
         next_a();
         next_c();
-        kstep(I1{}, [&](auto g_c) __attribute__((always_inline)) {
+        kstep(mode_c, I1{}, [&](auto g_c) __attribute__((always_inline)) {
             constexpr int g = decltype(g_c)::value;
             if constexpr (g >= START) {
                 spread(std::integral_constant<int, R>{}, std::integral_constant<int, STEPS - START>{},
                        std::integral_constant<int, g - START>{}, [&](auto r_c) __attribute__((always_inline)) { read(r_c, OTHER{}, I0{}); });
-                fill(s_c, std::integral_constant<int, g - START>{});
+                fill(mode_c, s_c, std::integral_constant<int, g - START>{});
             }
         });
-        kstep(I0{}, [&](auto g_c) __attribute__((always_inline)) {
+        bool far = false;
+        if constexpr (MODE == WG_FP16) far = get_flag(s_c);
+        kstep(mode_c, I0{}, [&](auto g_c) __attribute__((always_inline)) {
             constexpr int g = decltype(g_c)::value;
             if constexpr (g >= START)
                 spread(std::integral_constant<int, R>{}, std::integral_constant<int, STEPS - START>{},
                        std::integral_constant<int, g - START>{}, [&](auto r_c) __attribute__((always_inline)) { read(r_c, OTHER{}, I1{}); });
-            fill(s_c, std::integral_constant<int, STEPS + g - START>{});
+            fill(mode_c, s_c, std::integral_constant<int, STEPS + g - START>{});
         });
+        if (MODE == WG_FP16 && far && next < end) end = next;
     };
 
-    if (slabs != 0u) {
+    // Slabs [from, to) of this workgroup's; returns where it stopped (before
+    // `to` only in WG_FP16, at a slab that needs the split).
+    auto pipeline = [&](auto mode_c, uint32_t from, uint32_t to) __attribute__((always_inline)) -> uint32_t {
+        constexpr int MODE = decltype(mode_c)::value;
         // slabs 0 and 1 into the stages, the codes of slab 2 on their way
+        seek(from);
         next_a();
         static_for<0, NA>([&](auto q_c) __attribute__((always_inline)) { dma(q_c, I0{}); });
         next_a();
@@ -309,33 +372,60 @@ __global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void wgrad_kernel(WgradArgs
         static_for<0, 3 * NP>([&](auto i_c) __attribute__((always_inline)) { load_codes(I0{}, i_c); });
         next_c();
         static_for<0, 3 * NP>([&](auto i_c) __attribute__((always_inline)) { load_codes(I1{}, i_c); });
-        static_for<0, 4 * NP>([&](auto i_c) __attribute__((always_inline)) { convert(I0{}, I0{}, i_c); });
-        static_for<0, 4 * NP>([&](auto i_c) __attribute__((always_inline)) { convert(I1{}, I1{}, i_c); });
+        if constexpr (MODE == WG_FP16) {
+            put_flag(I0{});
+            put_flag(I1{});
+        }
+        static_for<0, 4 * NP>([&](auto i_c) __attribute__((always_inline)) { convert(mode_c, I0{}, i_c); });
+        static_for<0, 4 * NP>([&](auto i_c) __attribute__((always_inline)) { convert(mode_c, I1{}, i_c); });
         next_c();
         static_for<0, 3 * NP>([&](auto i_c) __attribute__((always_inline)) { load_codes(I0{}, i_c); });
         wait_vm<0>();
         lds_barrier();
+        uint32_t end = to;
+        if constexpr (MODE == WG_FP16) {
+            const bool far0 = get_flag(I0{}), far1 = get_flag(I1{});
+            lds_barrier();  // the flags are read before the first period's
+            if (far0) return from;
+            if (far1 && from + 1u < end) end = from + 1u;
+        }
         static_for<0, R>([&](auto r_c) __attribute__((always_inline)) { read(r_c, I0{}, I0{}); });
-        kstep(I0{}, [&](auto g_c) __attribute__((always_inline)) {
+        kstep(mode_c, I0{}, [&](auto g_c) __attribute__((always_inline)) {
             constexpr int g = decltype(g_c)::value;
             if constexpr (g >= START)
                 spread(std::integral_constant<int, R>{}, std::integral_constant<int, STEPS - START>{},
                        std::integral_constant<int, g - START>{}, [&](auto r_c) __attribute__((always_inline)) { read(r_c, I0{}, I1{}); });
         });
-        uint32_t k = 0;
-        for (; k + 2u < slabs; k += 2u) {
-            period(I0{});
-            period(I1{});
+        uint32_t k = from;
+        while (k + 1u < end) {
+            period(mode_c, I0{}, k + 2u, end);
+            if (++k + 1u >= end) break;
+            period(mode_c, I1{}, k + 2u, end);
+            ++k;
         }
-        if (k + 1u < slabs) period(I0{});
-        kstep(I1{}, [](auto) __attribute__((always_inline)) {});
+        kstep(mode_c, I1{}, [](auto) __attribute__((always_inline)) {});
         gap_nops();      // the last MFMAs have written their accumulators
-        wait_vm<0>();    // no DMA may still target LDS when the workgroup retires
+        wait_vm<0>();    // no DMA may still target LDS when the next pipeline starts or the workgroup retires
+        lds_barrier();
+        return end;
+    };
+
+    if constexpr (DT == DT_BF16) {
+        if (slabs != 0u) pipeline(std::integral_constant<int, WG_BF16>{}, 0u, slabs);
+    } else {
+        for (uint32_t at = 0; at < slabs;) {
+            at = pipeline(std::integral_constant<int, WG_FP16>{}, at, slabs);
+            if (at < slabs) {
+                const uint32_t to = slabs - at < kSplitSlabs ? slabs : at + kSplitSlabs;
+                pipeline(std::integral_constant<int, WG_SPLIT>{}, at, to);
+                at = to;
+            }
+        }
     }
 #pragma unroll
     for (int fm = 0; fm < FM; ++fm)
 #pragma unroll
-        for (int fn = 0; fn < FN; ++fn) asm volatile("" : "+a"(acc[fm][fn]));  // not read before the wait above
+        for (int fn = 0; fn < FN; ++fn) asm volatile("" : "+a"(acc[fm][fn]));  // not read before the gap above
 
     // ---- store: lane (lg, l16) of block pair t holds columns 32t + 8 lg + 0..7
     // of one row of dw; in odd lane groups the pair's halves change places ----
@@ -351,7 +441,11 @@ __global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void wgrad_kernel(WgradArgs
             const uint32_t n = n0 + wc * T::WN + 32u * t + 8u * lg;
             if (m >= out || n >= width) continue;
             const f32x4 x = acc[fm][2 * t], y = acc[fm][2 * t + 1];
-            const f32x4 a = swap ? y : x, b = swap ? x : y;
+            f32x4 a = swap ? y : x, b = swap ? x : y;
+            if constexpr (DT == DT_FP16) {
+                a *= 1.0f / (1 << kShift);
+                b *= 1.0f / (1 << kShift);
+            }
             const size_t at = (size_t)m * width + n;
             if (!whole || ODT == 4) {
                 float* p32 = (whole ? (float*)args.dw : part) + at;
