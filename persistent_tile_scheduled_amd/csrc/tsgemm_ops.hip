@@ -93,7 +93,7 @@ int tsgemm_layer_norm(int64_t rows, int64_t width, int dtype, int weight_dtype, 
     a.x = x; a.gamma = gamma; a.beta = beta; a.y = y; a.mean = mean; a.rstd = rstd;
     a.codes = static_cast<uint8_t*>(codes); a.scales = static_cast<uint8_t*>(scales);
     a.rows = rows; a.ldx = ldx; a.ldy = ldy; a.width = (uint32_t)width; a.wdt = weight_dtype;
-    a.eps = eps; a.inv_n = 1.0f / (float)width;
+    a.eps = eps; a.inv_n = 1.0 / (double)width;
     (void)hipGetLastError();
     tsg::launch_layer_norm(dtype, a, static_cast<hipStream_t>(stream));
     return launched("layer norm");
@@ -104,7 +104,8 @@ int64_t tsgemm_layer_norm_grad_workspace(int64_t rows, int64_t width) {
     const int rc = check_shape(rows, width);
     if (rc != TSGEMM_OK) return rc;
     if (width < 1) return fail(TSGEMM_EINVAL, "layer norm needs a width of at least 1");
-    return (int64_t)tsg::layer_norm_grad_groups(rows, (uint32_t)width) * 2 * grad_pitch(width) * (int64_t)sizeof(float);
+    // fp32 rows take as many workgroups as 16-bit ones or fewer
+    return (int64_t)tsg::layer_norm_grad_groups(TSGEMM_BF16, rows, (uint32_t)width) * 2 * grad_pitch(width) * (int64_t)sizeof(float);
 }
 
 int tsgemm_layer_norm_grad(int64_t rows, int64_t width, int dtype, int weight_dtype, const void* dy, int64_t lddy, const void* x,
@@ -141,8 +142,8 @@ int tsgemm_layer_norm_grad(int64_t rows, int64_t width, int dtype, int weight_dt
         if (rc != TSGEMM_OK) return rc;
     }
     if (!sums) return TSGEMM_OK;
-    tsg::launch_layer_norm_grad_sum(weight_dtype, part, tsg::layer_norm_grad_groups(rows, (uint32_t)width), grad_pitch(width),
-                                    (uint32_t)width, dgamma, dbeta, s);
+    tsg::launch_layer_norm_grad_sum(weight_dtype, part, tsg::layer_norm_grad_groups(dtype, rows, (uint32_t)width),
+                                    grad_pitch(width), (uint32_t)width, dgamma, dbeta, s);
     return launched("layer norm gradient sum");
 }
 

@@ -15,7 +15,7 @@ struct WgradArgs;
 void launch_layer_norm(int dt, const LnArgs& a, hipStream_t s);
 
 // Workgroups of a layer norm gradient: the count of partial sums per column.
-uint32_t layer_norm_grad_groups(int64_t rows, uint32_t width);
+uint32_t layer_norm_grad_groups(int dt, int64_t rows, uint32_t width);
 void launch_layer_norm_grad(int dt, const LnGradArgs& a, hipStream_t s);
 void launch_layer_norm_grad_sum(int wdt, const float* part, uint32_t groups, uint32_t pitch, uint32_t width, void* dgamma,
                                 void* dbeta, hipStream_t s);

@@ -10,7 +10,11 @@
 // 16-bit type): four neighbouring lanes hold an MX block of 32, whose largest
 // magnitude is a matter of two cross-lane moves inside the quad.  Rows need
 // only the alignment of their elements (gfx950 loads and stores 16 bytes at any
-// address); a chunk that the row's end cuts is loaded and stored value by value.
+// address).  A row that is not a multiple of 8 wide ends with a chunk that
+// reaches back over the one before (Chunks below): both lanes compute and store
+// the same values for the columns they share, and the sums count them once.
+// Against loads and stores of the cut chunk in pieces of 4, 2 and 1 values:
+// layer norm 20000 x 2501 bf16 67 -> 58 us.  Rows below 8 values have no other way.
 #pragma once
 
 #include "tsgemm_device.h"
@@ -23,6 +27,9 @@ typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));  // 16 bytes at a 2-byte boundary
+typedef uint32_t u32x2_any __attribute__((ext_vector_type(2), aligned(2)));
+typedef uint32_t u32_any __attribute__((aligned(2)));
+typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
 typedef short s16x2 __attribute__((ext_vector_type(2)));
 
 struct LnArgs {
@@ -37,7 +44,8 @@ struct LnArgs {
     int64_t rows, ldx, ldy;
     uint32_t width;
     int wdt;            // type of gamma and beta: the activation's or DT_FP32
-    float eps, inv_n;   // inv_n = 1 / width
+    float eps;
+    double inv_n;       // 1 / width
     uint32_t lpr;       // lanes per row (kernels with several rows per workgroup): 4 ... 64
 };
 
@@ -63,8 +71,9 @@ template <int DT> struct ElemBytes { static constexpr int v = DT == DT_FP32 ? 4 
 
 template <int DT> struct Chunk { u32x4 w[DT == DT_FP32 ? 2 : 1]; };  // 8 values as they lie in memory
 
-// The first `cnt` values of the chunk at p, zeros after them.
-template <int DT>
+// The first `cnt` values of the chunk at p, zeros after them.  A chunk that the
+// row's end cuts comes in pieces of 4, 2 and 1 values.  FULL: cnt is 8 or 0.
+template <int DT, bool FULL = false>
 __device__ __forceinline__ Chunk<DT> load_chunk(const char* p, int cnt) {
     Chunk<DT> c;
     constexpr int W = DT == DT_FP32 ? 2 : 1;
@@ -74,14 +83,33 @@ __device__ __forceinline__ Chunk<DT> load_chunk(const char* p, int cnt) {
     } else {
 #pragma unroll
         for (int i = 0; i < W; ++i) c.w[i] = u32x4{0u, 0u, 0u, 0u};
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            if (e < cnt) {
-                if constexpr (DT == DT_FP32)
-                    c.w[e / 4][e % 4] = *(const uint32_t*)(p + 4 * e);
-                else
-                    c.w[0][e / 2] |= (uint32_t)*(const uint16_t*)(p + 2 * e) << (16 * (e % 2));
+        if (FULL || cnt <= 0) return c;
+        if constexpr (DT == DT_FP32) {
+            u32x2 two = {0u, 0u};
+            uint32_t one = 0u;
+            if (cnt & 4) c.w[0] = *(const u32x4_any*)p;
+            if (cnt & 2) two = *(const u32x2_any*)(p + 4 * (cnt & 4));
+            if (cnt & 1) one = *(const uint32_t*)(p + 4 * (cnt & 6));
+            if (cnt & 4) c.w[1] = u32x4{cnt & 2 ? two.x : one, two.y, cnt & 2 ? one : 0u, 0u};
+            else c.w[0] = u32x4{cnt & 2 ? two.x : one, two.y, cnt & 2 ? one : 0u, 0u};
+        } else {
+            uint32_t two = 0u, one = 0u;
+            if (cnt & 4) {
+                const u32x2 v = *(const u32x2_any*)p;
+                c.w[0].x = v.x;
+                c.w[0].y = v.y;
             }
+            if (cnt & 2) two = *(const u32_any*)(p + 2 * (cnt & 4));
+            if (cnt & 1) one = *(const uint16_t*)(p + 2 * (cnt & 6));
+            const uint32_t first = cnt & 2 ? two : one, second = cnt & 2 ? one : 0u;
+            if (cnt & 4) {
+                c.w[0].z = first;
+                c.w[0].w = second;
+            } else {
+                c.w[0].x = first;
+                c.w[0].y = second;
+            }
+        }
     }
     return c;
 }
@@ -108,7 +136,7 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
         return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{a, b}), f16x2));
 }
 
-template <int DT>
+template <int DT, bool FULL = false>
 __device__ __forceinline__ void store_chunk(char* p, int cnt, const float* f) {
     u32x4 w[DT == DT_FP32 ? 2 : 1];
 #pragma unroll
@@ -121,28 +149,31 @@ __device__ __forceinline__ void store_chunk(char* p, int cnt, const float* f) {
     if (cnt == 8) {
 #pragma unroll
         for (int i = 0; i < (DT == DT_FP32 ? 2 : 1); ++i) *(u32x4_any*)(p + 16 * i) = w[i];
-    } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            if (e < cnt) {
-                if constexpr (DT == DT_FP32)
-                    *(uint32_t*)(p + 4 * e) = w[e / 4][e % 4];
-                else
-                    *(uint16_t*)(p + 2 * e) = (uint16_t)(w[0][e / 2] >> (16 * (e % 2)));
-            }
+    } else if (!FULL && cnt > 0) {
+        if constexpr (DT == DT_FP32) {
+            if (cnt & 4) *(u32x4_any*)p = w[0];
+            const u32x4 r = cnt & 4 ? w[1] : w[0];
+            if (cnt & 2) *(u32x2_any*)(p + 4 * (cnt & 4)) = u32x2{r.x, r.y};
+            if (cnt & 1) *(uint32_t*)(p + 4 * (cnt & 6)) = cnt & 2 ? r.z : r.x;
+        } else {
+            if (cnt & 4) *(u32x2_any*)p = u32x2{w[0].x, w[0].y};
+            const uint32_t first = cnt & 4 ? w[0].z : w[0].x, second = cnt & 4 ? w[0].w : w[0].y;
+            if (cnt & 2) *(u32_any*)(p + 2 * (cnt & 4)) = first;
+            if (cnt & 1) *(uint16_t*)(p + 2 * (cnt & 6)) = (uint16_t)(cnt & 2 ? second : first);
+        }
     }
 }
 
 // 8 weights from column `col`, of the activation's type or fp32; `fill` where there are none.
-template <int DT>
+template <int DT, bool FULL = false>
 __device__ __forceinline__ void load_weights(const void* w, int wdt, uint32_t col, int cnt, float fill, float* f) {
     if (w == nullptr || cnt <= 0) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) f[e] = fill;
     } else if (DT == DT_FP32 || wdt == DT_FP32) {
-        unpack<DT_FP32>(load_chunk<DT_FP32>((const char*)w + (size_t)col * 4u, cnt), f);
+        unpack<DT_FP32>(load_chunk<DT_FP32, FULL>((const char*)w + (size_t)col * 4u, cnt), f);
     } else {
-        unpack<DT>(load_chunk<DT>((const char*)w + (size_t)col * 2u, cnt), f);
+        unpack<DT>(load_chunk<DT, FULL>((const char*)w + (size_t)col * 2u, cnt), f);
     }
 }
 
@@ -155,7 +186,7 @@ __device__ __forceinline__ float dpp(float v) {
     const int b = __builtin_bit_cast(int, v);
     return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(b, b, CTRL, 0xF, 0xF, true));
 }
-constexpr int kQuadXor1 = 0xB1, kQuadXor2 = 0x4E, kHalfMirror = 0x141, kRowMirror = 0x140;
+constexpr int kQuadXor1 = 0xB1, kQuadXor2 = 0x4E, kHalfMirror = 0x141, kRowMirror = 0x140, kRowRotate8 = 0x128;
 
 __device__ __forceinline__ float add_rows16(float v) {
     const uint32_t b = __builtin_bit_cast(uint32_t, v);
@@ -179,20 +210,50 @@ __device__ __forceinline__ float group_sum(float v, uint32_t lanes) {
     return v;
 }
 
-// Sum over the workgroup's waves of K values each.  `slot`: 16 * K floats of
+// The same in fp64, for the forward statistics: a thread's own few values add up
+// in fp32, what crosses lanes in fp64.
+template <int CTRL>
+__device__ __forceinline__ double dpp(double v) {
+    const u32x2 b = __builtin_bit_cast(u32x2, v);
+    const u32x2 r = {__builtin_bit_cast(uint32_t, dpp<CTRL>(__builtin_bit_cast(float, (uint32_t)b.x))),
+                     __builtin_bit_cast(uint32_t, dpp<CTRL>(__builtin_bit_cast(float, (uint32_t)b.y)))};
+    return __builtin_bit_cast(double, r);
+}
+__device__ __forceinline__ double group_sum(double v, uint32_t lanes) {
+    v += dpp<kQuadXor1>(v);
+    v += dpp<kQuadXor2>(v);
+    if (lanes > 4u) v += dpp<kHalfMirror>(v);
+    if (lanes > 8u) v += dpp<kRowMirror>(v);
+    if (lanes > 16u) {
+        const u32x2 b = __builtin_bit_cast(u32x2, v);
+        const auto lo = __builtin_amdgcn_permlane16_swap(b.x, b.x, false, false);
+        const auto hi = __builtin_amdgcn_permlane16_swap(b.y, b.y, false, false);
+        v = __builtin_bit_cast(double, (u32x2{lo[0], hi[0]})) + __builtin_bit_cast(double, (u32x2{lo[1], hi[1]}));
+    }
+    if (lanes > 32u) {
+        const u32x2 b = __builtin_bit_cast(u32x2, v);
+        const auto lo = __builtin_amdgcn_permlane32_swap(b.x, b.x, false, false);
+        const auto hi = __builtin_amdgcn_permlane32_swap(b.y, b.y, false, false);
+        v = __builtin_bit_cast(double, (u32x2{lo[0], hi[0]})) + __builtin_bit_cast(double, (u32x2{lo[1], hi[1]}));
+    }
+    return v;
+}
+
+// Sum over the workgroup's waves of K values each.  `slot`: 16 * K values of
 // LDS, another than the previous call's (one barrier per call then suffices: a
 // wave reaches the next call's barrier only after it has read this call's slot).
-template <int K>
-__device__ __forceinline__ void block_sum(float (&v)[K], float* slot) {
+template <int K, class F>
+__device__ __forceinline__ void block_sum(F (&v)[K], F* slot) {
     const uint32_t wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+    float w1[K];
 #pragma unroll
-    for (int k = 0; k < K; ++k) v[k] = group_sum(v[k], 64u);
+    for (int k = 0; k < K; ++k) w1[k] = group_sum((float)v[k], 64u);
     if ((threadIdx.x & 63u) == 0u)
 #pragma unroll
-        for (int k = 0; k < K; ++k) slot[wave * K + k] = v[k];
+        for (int k = 0; k < K; ++k) slot[wave * K + k] = w1[k];
     lds_barrier();
 #pragma unroll
-    for (int k = 0; k < K; ++k) v[k] = 0.f;
+    for (int k = 0; k < K; ++k) v[k] = F(0);
     for (uint32_t w = 0; w < waves; ++w)
 #pragma unroll
         for (int k = 0; k < K; ++k) v[k] += slot[w * K + k];
@@ -224,12 +285,13 @@ __device__ __forceinline__ float quad_max(float m) {
 }
 
 // v: a quarter of a block per lane, the quad's lanes in order -> 8 codes; returns the scale's code.
-__device__ __forceinline__ uint32_t encode_chunk(float* v, u32x2& codes) {
+__device__ __forceinline__ uint32_t encode_chunk(const float* v, u32x2& codes) {
     float top = quad_max(max_abs8(v));
     const float inf = __builtin_inff();
     const bool odd = __builtin_amdgcn_ballot_w64(!(top < inf)) != 0u;  // wave-uniform, rare
     if (odd) {
         float m = 0.f;
+        asm volatile("" : "+v"(m));  // keeps this block a branch: computed for every chunk it would cost a third more
 #pragma unroll
         for (int e = 0; e < 8; ++e) m = __builtin_fmaxf(m, __builtin_fabsf(v[e]) < inf ? __builtin_fabsf(v[e]) : 0.f);
         top = quad_max(m);
@@ -237,21 +299,23 @@ __device__ __forceinline__ uint32_t encode_chunk(float* v, u32x2& codes) {
     const uint32_t field = __builtin_bit_cast(uint32_t, top) >> 23;
     const uint32_t scale = field > 8u ? field - 8u : 0u;
     const float lim = __builtin_bit_cast(float, ((scale + 8u) << 23) | 0x600000u);  // 448 * 2^(scale - 127)
-    if (odd) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            if (__builtin_fabsf(v[e]) < inf) v[e] = __builtin_amdgcn_fmed3f(v[e], -lim, lim);
-    } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = __builtin_amdgcn_fmed3f(v[e], -lim, lim);
-    }
     const float s = __builtin_bit_cast(float, scale << 23);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
+        float c[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) c[e] = __builtin_amdgcn_fmed3f(v[4 * i + e], -lim, lim);
         s16x2 r = {0, 0};
-        r = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(r, v[4 * i], v[4 * i + 1], s, false);
-        r = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(r, v[4 * i + 2], v[4 * i + 3], s, true);
+        r = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(r, c[0], c[1], s, false);
+        r = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(r, c[2], c[3], s, true);
         codes[i] = __builtin_bit_cast(uint32_t, r);
+    }
+    if (odd) {
+        uint32_t nan = 0x7Fu;
+        asm volatile("" : "+v"(nan));
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (!(__builtin_fabsf(v[e]) < inf)) codes[e / 4] |= nan << (8 * (e % 4));
     }
     return scale;
 }
@@ -274,13 +338,13 @@ __device__ __forceinline__ void decode_chunk(u32x2 codes, uint32_t scale, float*
 // layer norm, forward
 // ---------------------------------------------------------------------------
 // The chunk's part of a row, normalised, scaled and stored.
-template <int DT, bool CODES>
+template <int DT, bool CODES, bool FULL = false>
 __device__ __forceinline__ void ln_store(const LnArgs& a, int64_t row, uint32_t col, int cnt, float* v, float rstd,
                                          const float* g, const float* b) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = __builtin_fmaf(v[e] * rstd, g[e], b[e]);
     if (cnt > 0 && a.y != nullptr)
-        store_chunk<DT>((char*)a.y + ((size_t)row * a.ldy + col) * ElemBytes<DT>::v, cnt, v);
+        store_chunk<DT, FULL>((char*)a.y + ((size_t)row * a.ldy + col) * ElemBytes<DT>::v, cnt, v);
     if constexpr (CODES) {
         u32x2 c;
         const uint32_t s = encode_chunk(v, c);  // all lanes of a quad hold a chunk, or none does
@@ -291,12 +355,38 @@ __device__ __forceinline__ void ln_store(const LnArgs& a, int64_t row, uint32_t 
     }
 }
 
+// (sum of squares about the mean) / width + eps -> (...)^(-1/2)
+__device__ __forceinline__ float inverse_root(double v) { return (float)rsqrt(v); }
+
+// The chunks of a row that a thread works on: every T-th from its own.  FULL:
+// rows of 8 values or more; a chunk is there whole or not at all, and `skip` of
+// its first values are another lane's too (8: it is not there).  Else (one chunk
+// per row) cnt says how many values there are.
+template <int NC, bool FULL>
+struct Chunks {
+    uint32_t col[NC];
+    int cnt[NC], skip[NC];
+    __device__ __forceinline__ Chunks(uint32_t width, uint32_t t, uint32_t T) {
+#pragma unroll
+        for (int j = 0; j < NC; ++j) {
+            col[j] = (t + j * T) * 8u;
+            const int left = (int)width - (int)col[j];
+            cnt[j] = left <= 0 ? 0 : FULL || left > 8 ? 8 : left;
+            skip[j] = FULL ? (left <= 0 ? 8 : left < 8 ? 8 - left : 0) : 0;
+            if (FULL && skip[j] > 0 && skip[j] < 8) col[j] = width - 8u;
+        }
+    }
+    // f's values that this lane counts, zeros for the others
+    __device__ __forceinline__ float counted(int j, int e, float f) const { return FULL ? (e >= skip[j] ? f : 0.f) : (e < cnt[j] ? f : 0.f); }
+    __device__ __forceinline__ bool cut(int j) const { return FULL ? skip[j] != 0 : cnt[j] != 8; }
+};
+
 // One row per workgroup at a time, at most NC chunks per thread.  The row after
 // is requested before this one's sums, so that its latency passes behind them.
 // WAVES: several rows per workgroup of 256 threads, args.lpr lanes each.
-template <int DT, int NC, bool CODES, bool WAVES>
+template <int DT, int NC, bool CODES, bool WAVES, bool FULL>
 __global__ __launch_bounds__(WAVES ? 256 : 1024) void layer_norm_kernel(LnArgs a) {
-    __shared__ float slots[2][16];
+    __shared__ double slots[2][16];
     constexpr int EB = ElemBytes<DT>::v;
     const uint32_t T = WAVES ? a.lpr : blockDim.x;          // threads of a row
     const uint32_t t = WAVES ? threadIdx.x & (T - 1u) : threadIdx.x;
@@ -304,28 +394,18 @@ __global__ __launch_bounds__(WAVES ? 256 : 1024) void layer_norm_kernel(LnArgs a
     const int64_t step = (int64_t)gridDim.x * rows_wg;
     int64_t row = (int64_t)blockIdx.x * rows_wg + (WAVES ? threadIdx.x / T : 0u);
 
-    uint32_t col[NC];
-    int cnt[NC];
+    const Chunks<NC, FULL> c(a.width, t, T);
+    float g[NC][8], b[NC][8];
 #pragma unroll
     for (int j = 0; j < NC; ++j) {
-        col[j] = (t + j * T) * 8u;
-        const int left = (int)a.width - (int)col[j];
-        cnt[j] = left < 0 ? 0 : left > 8 ? 8 : left;
-    }
-    constexpr bool HOLD = NC <= 2;  // the weights stay in registers
-    float g[HOLD ? NC : 1][8], b[HOLD ? NC : 1][8];
-    if constexpr (HOLD) {
-#pragma unroll
-        for (int j = 0; j < NC; ++j) {
-            load_weights<DT>(a.gamma, a.wdt, col[j], cnt[j], 1.f, g[j]);
-            load_weights<DT>(a.beta, a.wdt, col[j], cnt[j], 0.f, b[j]);
-        }
+        load_weights<DT, FULL>(a.gamma, a.wdt, c.col[j], c.cnt[j], 1.f, g[j]);
+        load_weights<DT, FULL>(a.beta, a.wdt, c.col[j], c.cnt[j], 0.f, b[j]);
     }
     Chunk<DT> next[NC];
     auto fetch = [&](int64_t r) __attribute__((always_inline)) {
 #pragma unroll
         for (int j = 0; j < NC; ++j)
-            next[j] = load_chunk<DT>((const char*)a.x + ((size_t)r * a.ldx + col[j]) * EB, r < a.rows ? cnt[j] : 0);
+            next[j] = load_chunk<DT, FULL>((const char*)a.x + ((size_t)r * a.ldx + c.col[j]) * EB, r < a.rows ? c.cnt[j] : 0);
     };
     fetch(row);
     // the count of rounds is the workgroup's: lanes without a row go along
@@ -335,29 +415,42 @@ __global__ __launch_bounds__(WAVES ? 256 : 1024) void layer_norm_kernel(LnArgs a
         for (int j = 0; j < NC; ++j) unpack<DT>(next[j], v[j]);
         fetch(row + step);
 
-        float s[1] = {0.f};
-#pragma unroll
-        for (int j = 0; j < NC; ++j)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) s[0] += v[j][e];
-        if constexpr (WAVES) s[0] = group_sum(s[0], T);
-        else block_sum<1>(s, slots[0]);
-        const float mean = s[0] * a.inv_n;
-        s[0] = 0.f;
+        double s[1];
+        float part = 0.f;
 #pragma unroll
         for (int j = 0; j < NC; ++j) {
+            float p = ((v[j][0] + v[j][1]) + (v[j][2] + v[j][3])) + ((v[j][4] + v[j][5]) + (v[j][6] + v[j][7]));
+            if (c.cut(j)) {
+                p = 0.f;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[j][e] -= mean;
-            if (cnt[j] < 8) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) v[j][e] = e < cnt[j] ? v[j][e] : 0.f;
+                for (int e = 0; e < 8; ++e) p += c.counted(j, e, v[j][e]);
             }
-#pragma unroll
-            for (int e = 0; e < 8; ++e) s[0] = __builtin_fmaf(v[j][e], v[j][e], s[0]);
+            part += p;
         }
+        s[0] = part;
+        if constexpr (WAVES) s[0] = group_sum(s[0], T);
+        else block_sum<1>(s, slots[0]);
+        const float mean = (float)(s[0] * a.inv_n);
+        part = 0.f;
+#pragma unroll
+        for (int j = 0; j < NC; ++j) {
+            float q = 0.f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                v[j][e] -= mean;
+                q = __builtin_fmaf(v[j][e], v[j][e], q);
+            }
+            if (c.cut(j)) {
+                q = 0.f;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) q = __builtin_fmaf(c.counted(j, e, v[j][e]), v[j][e], q);
+            }
+            part += q;
+        }
+        s[0] = part;
         if constexpr (WAVES) s[0] = group_sum(s[0], T);
         else block_sum<1>(s, slots[1]);
-        const float rstd = rsqrtf(__builtin_fmaf(s[0], a.inv_n, a.eps));
+        const float rstd = inverse_root(s[0] * a.inv_n + (double)a.eps);
 
         const bool live = row < a.rows;
         if (t == 0u && live && a.mean != nullptr) {
@@ -365,15 +458,8 @@ __global__ __launch_bounds__(WAVES ? 256 : 1024) void layer_norm_kernel(LnArgs a
             a.rstd[row] = rstd;
         }
 #pragma unroll
-        for (int j = 0; j < NC; ++j) {
-            if constexpr (HOLD) {
-                ln_store<DT, CODES>(a, row, col[j], live ? cnt[j] : 0, v[j], rstd, g[j], b[j]);
-            } else {
-                load_weights<DT>(a.gamma, a.wdt, col[j], cnt[j], 1.f, g[0]);
-                load_weights<DT>(a.beta, a.wdt, col[j], cnt[j], 0.f, b[0]);
-                ln_store<DT, CODES>(a, row, col[j], live ? cnt[j] : 0, v[j], rstd, g[0], b[0]);
-            }
-        }
+        for (int j = 0; j < NC; ++j)
+            ln_store<DT, CODES, FULL>(a, row, c.col[j], live ? c.cnt[j] : 0, v[j], rstd, g[j], b[j]);
     }
 }
 
@@ -381,29 +467,32 @@ __global__ __launch_bounds__(WAVES ? 256 : 1024) void layer_norm_kernel(LnArgs a
 // times (the second and third time mostly out of a cache).
 template <int DT, bool CODES>
 __global__ __launch_bounds__(1024) void layer_norm_wide_kernel(LnArgs a) {
-    __shared__ float slots[2][16];
+    __shared__ double slots[2][16];
     constexpr int EB = ElemBytes<DT>::v;
     const uint32_t rounds = (a.width + 8191u) / 8192u;
     for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
         const char* x = (const char*)a.x + (size_t)row * a.ldx * EB;
-        float s[1] = {0.f}, mean = 0.f, v[8];
+        double s[1] = {0.0};
+        float mean = 0.f, v[8];
         for (uint32_t i = 0; i < 2u * rounds; ++i) {  // first the sum, then the squares about the mean
             if (i == rounds) {
                 block_sum<1>(s, slots[0]);
-                mean = s[0] * a.inv_n;
-                s[0] = 0.f;
+                mean = (float)(s[0] * a.inv_n);
+                s[0] = 0.0;
             }
             const uint32_t col = (threadIdx.x + 1024u * (i % rounds)) * 8u;
             const int cnt = col >= a.width ? 0 : a.width - col < 8u ? (int)(a.width - col) : 8;
             unpack<DT>(load_chunk<DT>(x + (size_t)col * EB, cnt), v);
+            float part = 0.f;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const float d = e < cnt ? v[e] - mean : 0.f;
-                s[0] = i < rounds ? s[0] + d : __builtin_fmaf(d, d, s[0]);
+                part = i < rounds ? part + d : __builtin_fmaf(d, d, part);
             }
+            s[0] += part;
         }
         block_sum<1>(s, slots[1]);
-        const float rstd = rsqrtf(__builtin_fmaf(s[0], a.inv_n, a.eps));
+        const float rstd = inverse_root(s[0] * a.inv_n + (double)a.eps);
         if (threadIdx.x == 0u && a.mean != nullptr) {
             a.mean[row] = mean;
             a.rstd[row] = rstd;
@@ -428,92 +517,122 @@ __global__ __launch_bounds__(1024) void layer_norm_wide_kernel(LnArgs a) {
 // A thread keeps its columns' sums over the workgroup's rows in registers; the
 // workgroups' sums meet in a second, small launch in a fixed order.
 // ---------------------------------------------------------------------------
-template <int DT, int NC, bool WAVES>
+// AHEAD rows are on their way while one is worked on.  With two chunks per
+// thread and row (RAW) a row is kept as it was read and unpacked twice.
+template <int DT, int NC, bool WAVES, bool FULL, int AHEAD>
 __global__ __launch_bounds__(WAVES ? 256 : 1024) void layer_norm_grad_kernel(LnGradArgs a) {
     __shared__ float slots[2][32];
     __shared__ float sums[WAVES ? 256 * 8 : 1];
     constexpr int EB = ElemBytes<DT>::v;
+    constexpr bool RAW = !WAVES && NC > 1;
     const uint32_t T = WAVES ? a.lpr : blockDim.x;
     const uint32_t t = WAVES ? threadIdx.x & (T - 1u) : threadIdx.x;
     const uint32_t rows_wg = WAVES ? 256u / T : 1u;
     const int64_t step = (int64_t)gridDim.x * rows_wg;
     int64_t row = (int64_t)blockIdx.x * rows_wg + (WAVES ? threadIdx.x / T : 0u);
 
-    uint32_t col[NC];
-    int cnt[NC];
-    float gam[NC][8], dg[NC][8], db[NC][8];
+    const Chunks<NC, FULL> c(a.width, t, T);
+    float gam[RAW ? 1 : NC][8], dg[NC][8], db[NC][8];
 #pragma unroll
     for (int j = 0; j < NC; ++j) {
-        col[j] = (t + j * T) * 8u;
-        const int left = (int)a.width - (int)col[j];
-        cnt[j] = left < 0 ? 0 : left > 8 ? 8 : left;
-        load_weights<DT>(a.gamma, a.wdt, col[j], cnt[j], 1.f, gam[j]);
+        if constexpr (!RAW) load_weights<DT, FULL>(a.gamma, a.wdt, c.col[j], c.cnt[j], 1.f, gam[j]);
 #pragma unroll
         for (int e = 0; e < 8; ++e) dg[j][e] = db[j][e] = 0.f;
     }
-    Chunk<DT> nx[NC], nd[NC];
-    float n_mean = 0.f, n_rstd = 0.f;
-    auto fetch = [&](int64_t r) __attribute__((always_inline)) {
+    struct Row {
+        Chunk<DT> x[NC], dy[NC];
+        float mean, rstd;
+    };
+    auto fetch = [&](Row& n, int64_t r) __attribute__((always_inline)) {
         const bool live = r < a.rows;
-        n_mean = live ? a.mean[r] : 0.f;
-        n_rstd = live ? a.rstd[r] : 0.f;
+        n.mean = live ? a.mean[r] : 0.f;
+        n.rstd = live ? a.rstd[r] : 0.f;
 #pragma unroll
         for (int j = 0; j < NC; ++j) {
-            nx[j] = load_chunk<DT>((const char*)a.x + ((size_t)r * a.ldx + col[j]) * EB, live ? cnt[j] : 0);
-            nd[j] = load_chunk<DT>((const char*)a.dy + ((size_t)r * a.lddy + col[j]) * EB, live ? cnt[j] : 0);
+            n.x[j] = load_chunk<DT, FULL>((const char*)a.x + ((size_t)r * a.ldx + c.col[j]) * EB, live ? c.cnt[j] : 0);
+            n.dy[j] = load_chunk<DT, FULL>((const char*)a.dy + ((size_t)r * a.lddy + c.col[j]) * EB, live ? c.cnt[j] : 0);
         }
     };
-    fetch(row);
     uint32_t slot = 0;
-    for (int64_t base = (int64_t)blockIdx.x * rows_wg; base < a.rows; base += step, row += step, slot ^= 1u) {
-        float h[NC][8], g[NC][8];
-        const float mean = n_mean, rstd = n_rstd;
+    // where no chunk is, dy is 0, and so are g, g h and dy h (mean and rstd that
+    // are no numbers only reach columns that are not stored)
+    auto open = [&](const Row& n, int j, float mean, float rstd, float* h, float* d) __attribute__((always_inline)) {
+        unpack<DT>(n.x[j], h);
+        unpack<DT>(n.dy[j], d);
 #pragma unroll
-        for (int j = 0; j < NC; ++j) {
-            unpack<DT>(nx[j], h[j]);
-            unpack<DT>(nd[j], g[j]);
-        }
-        fetch(row + step);
+        for (int e = 0; e < 8; ++e) h[e] = (h[e] - mean) * rstd;
+    };
+    auto work = [&](Row& n) __attribute__((always_inline)) {
+        float h[RAW ? 1 : NC][8], g[RAW ? 1 : NC][8];
+        const float mean = n.mean, rstd = n.rstd;
         float s[2] = {0.f, 0.f};
-#pragma unroll
-        for (int j = 0; j < NC; ++j)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                // past the row's end dy is 0, and so are g, g h and dy h (mean and rstd
-                // that are no numbers only reach columns that are not stored)
-                const float d = g[j][e];
-                h[j][e] = (h[j][e] - mean) * rstd;
-                dg[j][e] = __builtin_fmaf(d, h[j][e], dg[j][e]);
-                db[j][e] += d;
-                g[j][e] = d * gam[j][e];
-            }
+        Row kept;
+        if constexpr (RAW) kept = n;
 #pragma unroll
         for (int j = 0; j < NC; ++j) {
-            if (cnt[j] < 8) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) h[j][e] = e < cnt[j] ? h[j][e] : 0.f;
-            }
+            const int k = RAW ? 0 : j;
+            open(n, j, mean, rstd, h[k], g[k]);
+            if constexpr (RAW) load_weights<DT, FULL>(a.gamma, a.wdt, c.col[j], c.cnt[j], 1.f, gam[0]);
+            float p0 = 0.f, p1 = 0.f;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                s[0] += g[j][e];
-                s[1] = __builtin_fmaf(g[j][e], h[j][e], s[1]);
+                const float d = g[k][e];
+                dg[j][e] = __builtin_fmaf(d, h[k][e], dg[j][e]);
+                db[j][e] += d;
+                g[k][e] = d * gam[k][e];
+                p0 += g[k][e];
+                p1 = __builtin_fmaf(g[k][e], h[k][e], p1);
             }
+            if (c.cut(j)) {
+                p0 = p1 = 0.f;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    p0 += c.counted(j, e, g[k][e]);
+                    p1 += c.counted(j, e, g[k][e] * h[k][e]);
+                }
+            }
+            s[0] += p0;
+            s[1] += p1;
         }
+        fetch(n, row + AHEAD * step);
         if constexpr (WAVES) {
             s[0] = group_sum(s[0], T);
             s[1] = group_sum(s[1], T);
         } else {
             block_sum<2>(s, slots[slot]);
+            slot ^= 1u;
         }
         const float c1 = -rstd * (s[0] * a.inv_n), c2 = -rstd * (s[1] * a.inv_n);
         if (row < a.rows) {
 #pragma unroll
             for (int j = 0; j < NC; ++j) {
+                const int k = RAW ? 0 : j;
+                if constexpr (RAW) {
+                    open(kept, j, mean, rstd, h[0], g[0]);
+                    load_weights<DT, FULL>(a.gamma, a.wdt, c.col[j], c.cnt[j], 1.f, gam[0]);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) g[0][e] *= gam[0][e];
+                }
                 float o[8];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) o[e] = __builtin_fmaf(rstd, g[j][e], __builtin_fmaf(c2, h[j][e], c1));
-                if (cnt[j] > 0) store_chunk<DT>((char*)a.dx + ((size_t)row * a.lddx + col[j]) * EB, cnt[j], o);
+                for (int e = 0; e < 8; ++e) o[e] = __builtin_fmaf(rstd, g[k][e], __builtin_fmaf(c2, h[k][e], c1));
+                if (c.cnt[j] > 0) store_chunk<DT, FULL>((char*)a.dx + ((size_t)row * a.lddx + c.col[j]) * EB, c.cnt[j], o);
             }
+        }
+        row += step;
+    };
+    Row n[AHEAD];
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) fetch(n[i], row + i * step);
+    // the count of rounds is the workgroup's: lanes without a row go along
+    int64_t base = (int64_t)blockIdx.x * rows_wg;
+    while (base < a.rows) {
+        work(n[0]);
+        base += step;
+        if constexpr (AHEAD > 1) {
+            if (base >= a.rows) break;
+            work(n[1]);
+            base += step;
         }
     }
     if (a.part == nullptr) return;
@@ -534,12 +653,12 @@ __global__ __launch_bounds__(WAVES ? 256 : 1024) void layer_norm_grad_kernel(LnG
                     const uint32_t e = o / T, lane = o & (T - 1u);
                     float s = 0.f;
                     for (uint32_t r = 0; r < rows_wg; ++r) s += sums[e * 256u + r * T + lane];
-                    const uint32_t c = (lane + j * T) * 8u + e;
-                    if (c < a.pitch) part[k * a.pitch + c] = s;
+                    const Chunks<NC, FULL> of(a.width, lane, T);
+                    if (of.cnt[j] > 0) part[k * a.pitch + of.col[j] + e] = s;
                 }
-            } else if (cnt[j] > 0) {  // the pitch is a multiple of 8
-                *(f32x4*)(part + k * a.pitch + col[j]) = f32x4{v[0], v[1], v[2], v[3]};
-                *(f32x4*)(part + k * a.pitch + col[j] + 4) = f32x4{v[4], v[5], v[6], v[7]};
+            } else if (c.cnt[j] > 0) {
+                *(f32x4_any*)(part + k * a.pitch + c.col[j]) = f32x4{v[0], v[1], v[2], v[3]};
+                *(f32x4_any*)(part + k * a.pitch + c.col[j] + 4) = f32x4{v[4], v[5], v[6], v[7]};
             }
         }
 }
@@ -594,38 +713,45 @@ __global__ __launch_bounds__(1024) void layer_norm_grad_wide_kernel(LnGradArgs a
     }
 }
 
-// dgamma and dbeta from the workgroups' sums: 64 columns per workgroup, the
-// sums split over its 16 waves, each adding its share in order.  `groups` may be
-// 0 (no rows): the gradients are then 0.
+// dgamma and dbeta from the workgroups' sums: 32 columns per workgroup, 4 per
+// lane, so that a wave reads 8 workgroups' sums at once; the lanes' and the 16
+// waves' shares meet in a fixed order.  `groups` may be 0 (no rows): the
+// gradients are then 0.
 template <int WDT>
 __global__ __launch_bounds__(1024) void layer_norm_grad_sum_kernel(const float* part, uint32_t groups, uint32_t pitch,
                                                                    uint32_t width, void* dgamma, void* dbeta) {
-    __shared__ float sums[2][16][64];
+    __shared__ float sums[2][16][32];
     const uint32_t lane = threadIdx.x & 63u, wave = threadIdx.x >> 6;
-    const uint32_t c = blockIdx.x * 64u + lane;
-    float s[2] = {0.f, 0.f};
-    if (c < width) {
-        const uint32_t each = (groups + 15u) / 16u;
-        const uint32_t end = (wave + 1u) * each < groups ? (wave + 1u) * each : groups;
-#pragma unroll 8
-        for (uint32_t g = wave * each; g < end; ++g) {
+    const uint32_t c = blockIdx.x * 32u + (lane & 7u) * 4u;
+    f32x4 s[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+    if (c < pitch) {
+#pragma unroll 4
+        for (uint32_t g = wave * 8u + (lane >> 3); g < groups; g += 128u) {
             const float* p = part + (size_t)g * 2u * pitch + c;
-            s[0] += p[0];
-            s[1] += p[pitch];
+            s[0] += *(const f32x4*)p;
+            s[1] += *(const f32x4*)(p + pitch);
         }
     }
-    sums[0][wave][lane] = s[0];
-    sums[1][wave][lane] = s[1];
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            float v = s[k][e];
+            v += dpp<kRowRotate8>(v);
+            v = add_rows32(add_rows16(v));
+            if (lane < 8u) sums[k][wave][lane * 4u + e] = v;
+        }
     lds_barrier();
-    if (wave < 2u && c < width) {
+    if (threadIdx.x < 64u) {
+        const uint32_t k = threadIdx.x >> 5, at = blockIdx.x * 32u + (threadIdx.x & 31u);
         float v = 0.f;
 #pragma unroll
-        for (int w = 0; w < 16; ++w) v += sums[wave][w][lane];
-        void* out = wave == 0u ? dgamma : dbeta;
-        if (out != nullptr) {
-            if constexpr (WDT == DT_FP32) ((float*)out)[c] = v;
-            else if constexpr (WDT == DT_BF16) ((__bf16*)out)[c] = (__bf16)v;
-            else ((_Float16*)out)[c] = (_Float16)v;
+        for (int w = 0; w < 16; ++w) v += sums[k][w][threadIdx.x & 31u];
+        void* out = k == 0u ? dgamma : dbeta;
+        if (out != nullptr && at < width) {
+            if constexpr (WDT == DT_FP32) ((float*)out)[at] = v;
+            else if constexpr (WDT == DT_BF16) ((__bf16*)out)[at] = (__bf16)v;
+            else ((_Float16*)out)[at] = (_Float16)v;
         }
     }
 }

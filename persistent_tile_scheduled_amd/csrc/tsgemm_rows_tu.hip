@@ -8,17 +8,18 @@ namespace {
 
 constexpr uint32_t kCus = 256;  // MI355X
 
-// Which kernel a row of `width` values takes.  Up to 512 * kWaveChunks values a
-// row belongs to a part of a wave (or a whole one): its sums need no barrier.
-// Wider rows take a workgroup with two chunks per thread (the gradient, which
-// also holds its columns' sums, one while it can), or (forward only) four;
-// still wider ones are read in several rounds.
-enum RowClass { ROW_WAVE1, ROW_WAVE2, ROW_BLOCK1, ROW_BLOCK2, ROW_BLOCK4, ROW_WIDE };
+// Which kernel a row of `width` values takes.  Up to 512 values per wave and
+// chunk a row belongs to a part of a wave (or a whole one): its sums need no
+// barrier.  Wider rows take a workgroup with two chunks per thread (the
+// gradient, which also holds its columns' sums, one while it can); still wider
+// ones are read in several rounds.
+enum RowClass { ROW_WAVE1, ROW_WAVE2, ROW_BLOCK1, ROW_BLOCK2, ROW_WIDE };
 
 struct RowShape {
     RowClass cls;
     uint32_t threads;  // of a workgroup
     uint32_t lpr;      // lanes per row of the wave classes
+    uint32_t rows;     // of a workgroup at a time
 };
 
 RowShape row_shape(uint32_t width, bool grad) {
@@ -26,43 +27,75 @@ RowShape row_shape(uint32_t width, bool grad) {
     if (chunks <= 64u) {
         uint32_t lpr = 4;
         while (lpr < chunks) lpr *= 2;
-        return {ROW_WAVE1, 256, lpr};
+        return {ROW_WAVE1, 256, lpr, 256u / lpr};
     }
-    if (chunks <= 128u) return {ROW_WAVE2, 256, 64};
-    if (grad && chunks <= 1024u) return {ROW_BLOCK1, (chunks + 63u) / 64u * 64u, 64};
-    if (chunks <= 2048u) return {ROW_BLOCK2, (chunks + 127u) / 128u * 64u, 64};
-    if (chunks <= 4096u && !grad) return {ROW_BLOCK4, 1024, 64};
-    return {ROW_WIDE, 1024, 64};
+    if (chunks <= 128u) return {ROW_WAVE2, 256, 64, 4};
+    if (grad && chunks <= 1024u) return {ROW_BLOCK1, (chunks + 63u) / 64u * 64u, 64, 1};
+    if (chunks <= 2048u) return {ROW_BLOCK2, (chunks + 127u) / 128u * 64u, 64, 1};
+    return {ROW_WIDE, 1024, 64, 1};
 }
 
 uint32_t at_most(int64_t n, uint32_t most) { return n < (int64_t)most ? (uint32_t)n : most; }
 
-// Workgroups that stay: as many as find room on the chip at once.
-uint32_t row_groups(const RowShape& r, int64_t rows) {
-    const int64_t per = r.cls <= ROW_WAVE2 ? 256 / r.lpr : 1;
-    return at_most((rows + per - 1) / per, kCus * (2048u / r.threads));
+// Workgroups that stay, per compute unit: as many as hold 32 KiB of rows at a
+// time (with as much again on its way), at most what finds room at once.  Fewer
+// leave memory idle, more make it jump between more rows: layer norm 8192 x 8192
+// bf16 with 1, 2, 4 and 8 workgroups 62, 51, 52 and 55 us, 60000 x 1024 with 2, 4, 8 and
+// 16 52, 48, 53 and 51 us.
+uint32_t groups_per_cu(const RowShape& r, uint32_t width, int element, uint32_t matrices, uint32_t most) {
+    const uint64_t held = (uint64_t)r.rows * width * (uint32_t)element * matrices;
+    const uint64_t n = (32768u + held / 2u) / held, room = 2048u / r.threads < most ? 2048u / r.threads : most;
+    return n < 1u ? 1u : n < room ? (uint32_t)n : (uint32_t)room;
+}
+
+uint32_t row_groups(const RowShape& r, int64_t rows, uint32_t per_cu) {
+    return at_most((rows + r.rows - 1) / r.rows, kCus * per_cu);
 }
 
 template <int DT, bool CODES>
 void layer_norm_of(const LnArgs& a, const RowShape& r, hipStream_t s) {
-    const dim3 grid(row_groups(r, a.rows)), block(r.threads);
+    const dim3 grid(row_groups(r, a.rows, groups_per_cu(r, a.width, ElemBytes<DT>::v, 1u, 8u))), block(r.threads);
+    if (a.width < 8u) {
+        if constexpr (!CODES) hipLaunchKernelGGL((layer_norm_kernel<DT, 1, false, true, false>), grid, block, 0, s, a);
+        return;
+    }
     switch (r.cls) {
-        case ROW_WAVE1: hipLaunchKernelGGL((layer_norm_kernel<DT, 1, CODES, true>), grid, block, 0, s, a); break;
-        case ROW_WAVE2: hipLaunchKernelGGL((layer_norm_kernel<DT, 2, CODES, true>), grid, block, 0, s, a); break;
-        case ROW_BLOCK2: hipLaunchKernelGGL((layer_norm_kernel<DT, 2, CODES, false>), grid, block, 0, s, a); break;
-        case ROW_BLOCK4: hipLaunchKernelGGL((layer_norm_kernel<DT, 4, CODES, false>), grid, block, 0, s, a); break;
+        case ROW_WAVE1: hipLaunchKernelGGL((layer_norm_kernel<DT, 1, CODES, true, true>), grid, block, 0, s, a); break;
+        case ROW_WAVE2: hipLaunchKernelGGL((layer_norm_kernel<DT, 2, CODES, true, true>), grid, block, 0, s, a); break;
+        case ROW_BLOCK2: hipLaunchKernelGGL((layer_norm_kernel<DT, 2, CODES, false, true>), grid, block, 0, s, a); break;
         default: hipLaunchKernelGGL((layer_norm_wide_kernel<DT, CODES>), grid, block, 0, s, a); break;
     }
 }
 
 template <int DT>
+void layer_norm_to(const LnArgs& a, const RowShape& r, hipStream_t s) {
+    a.codes != nullptr ? layer_norm_of<DT, true>(a, r, s) : layer_norm_of<DT, false>(a, r, s);
+}
+
+// The gradient reads two matrices, and each workgroup leaves sums of its own:
+// at most three workgroups (65536 x 256 bf16 with 2, 3 and 4: 28.4, 27.5 and
+// 29.7 us).
+uint32_t grad_per_cu(const RowShape& r, uint32_t width, int element) { return groups_per_cu(r, width, element, 2u, 3u); }
+
+template <int DT>
 void layer_norm_grad_of(const LnGradArgs& a, const RowShape& r, hipStream_t s) {
-    const dim3 grid(layer_norm_grad_groups(a.rows, a.width)), block(r.threads);
+    const uint32_t per_cu = grad_per_cu(r, a.width, ElemBytes<DT>::v);
+    const dim3 grid(row_groups(r, a.rows, per_cu)), block(r.threads);
+    if (a.width < 8u) {
+        hipLaunchKernelGGL((layer_norm_grad_kernel<DT, 1, true, false, 1>), grid, block, 0, s, a);
+        return;
+    }
     switch (r.cls) {
-        case ROW_WAVE1: hipLaunchKernelGGL((layer_norm_grad_kernel<DT, 1, true>), grid, block, 0, s, a); break;
-        case ROW_WAVE2: hipLaunchKernelGGL((layer_norm_grad_kernel<DT, 2, true>), grid, block, 0, s, a); break;
-        case ROW_BLOCK1: hipLaunchKernelGGL((layer_norm_grad_kernel<DT, 1, false>), grid, block, 0, s, a); break;
-        case ROW_BLOCK2: hipLaunchKernelGGL((layer_norm_grad_kernel<DT, 2, false>), grid, block, 0, s, a); break;
+        case ROW_WAVE1: hipLaunchKernelGGL((layer_norm_grad_kernel<DT, 1, true, true, 1>), grid, block, 0, s, a); break;
+        case ROW_WAVE2: hipLaunchKernelGGL((layer_norm_grad_kernel<DT, 2, true, true, 1>), grid, block, 0, s, a); break;
+        case ROW_BLOCK1:
+            // a workgroup alone on its compute unit asks for two rows ahead:
+            // 8192 x 8192 bf16 87.2 -> 84.0 us; with two or more there is
+            // nothing to gain (16000 x 4000 fp16 77.3 -> 79.7)
+            if (per_cu == 1u) hipLaunchKernelGGL((layer_norm_grad_kernel<DT, 1, false, true, 2>), grid, block, 0, s, a);
+            else hipLaunchKernelGGL((layer_norm_grad_kernel<DT, 1, false, true, 1>), grid, block, 0, s, a);
+            break;
+        case ROW_BLOCK2: hipLaunchKernelGGL((layer_norm_grad_kernel<DT, 2, false, true, 1>), grid, block, 0, s, a); break;
         default: hipLaunchKernelGGL((layer_norm_grad_wide_kernel<DT>), grid, block, 0, s, a); break;
     }
 }
@@ -75,16 +108,14 @@ void launch_layer_norm(int dt, const LnArgs& args, hipStream_t s) {
     LnArgs a = args;
     const RowShape r = row_shape(a.width, false);
     a.lpr = r.lpr;
-    const bool codes = a.codes != nullptr;
-    if (dt == DT_FP16) codes ? layer_norm_of<DT_FP16, true>(a, r, s) : layer_norm_of<DT_FP16, false>(a, r, s);
-    else if (dt == DT_BF16) codes ? layer_norm_of<DT_BF16, true>(a, r, s) : layer_norm_of<DT_BF16, false>(a, r, s);
-    else codes ? layer_norm_of<DT_FP32, true>(a, r, s) : layer_norm_of<DT_FP32, false>(a, r, s);
+    if (dt == DT_FP16) layer_norm_to<DT_FP16>(a, r, s);
+    else if (dt == DT_BF16) layer_norm_to<DT_BF16>(a, r, s);
+    else layer_norm_to<DT_FP32>(a, r, s);
 }
 
-uint32_t layer_norm_grad_groups(int64_t rows, uint32_t width) {
+uint32_t layer_norm_grad_groups(int dt, int64_t rows, uint32_t width) {
     const RowShape r = row_shape(width, true);
-    const int64_t per = r.cls <= ROW_WAVE2 ? 256 / r.lpr : 1;
-    return at_most((rows + per - 1) / per, kCus * (r.threads > 512u ? 1u : 2u));
+    return row_groups(r, rows, grad_per_cu(r, width, dt == DT_FP32 ? 4 : 2));
 }
 
 void launch_layer_norm_grad(int dt, const LnGradArgs& args, hipStream_t s) {
@@ -98,7 +129,7 @@ void launch_layer_norm_grad(int dt, const LnGradArgs& args, hipStream_t s) {
 
 void launch_layer_norm_grad_sum(int wdt, const float* part, uint32_t groups, uint32_t pitch, uint32_t width, void* dgamma,
                                 void* dbeta, hipStream_t s) {
-    const dim3 grid((width + 63u) / 64u), block(1024);
+    const dim3 grid((width + 31u) / 32u), block(1024);
     if (wdt == DT_FP16)
         hipLaunchKernelGGL((layer_norm_grad_sum_kernel<DT_FP16>), grid, block, 0, s, part, groups, pitch, width, dgamma, dbeta);
     else if (wdt == DT_BF16)
