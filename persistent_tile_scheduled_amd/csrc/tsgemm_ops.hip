@@ -130,18 +130,20 @@ int tsgemm_layer_norm_grad(int64_t rows, int64_t width, int dtype, int weight_dt
             return fail(TSGEMM_EINVAL, "dgamma and dbeta need a 16-byte aligned workspace of %lld bytes", (long long)need);
     }
     const hipStream_t s = static_cast<hipStream_t>(stream);
-    float* part = sums ? static_cast<float*>(workspace) : nullptr;
+    const bool small = rows > 0 && tsg::layer_norm_grad_small(rows, (uint32_t)width);
+    float* part = sums && !small ? static_cast<float*>(workspace) : nullptr;
     (void)hipGetLastError();
     if (rows > 0) {
         tsg::LnGradArgs a = {};
         a.dy = dy; a.x = x; a.gamma = gamma; a.mean = mean; a.rstd = rstd; a.dx = dx; a.part = part;
         a.rows = rows; a.lddy = lddy; a.ldx = ldx; a.lddx = lddx;
         a.width = (uint32_t)width; a.pitch = grad_pitch(width); a.wdt = weight_dtype; a.inv_n = 1.0f / (float)width;
+        if (small) { a.dgamma = dgamma; a.dbeta = dbeta; }
         tsg::launch_layer_norm_grad(dtype, a, s);
         rc = launched("layer norm gradient");
         if (rc != TSGEMM_OK) return rc;
     }
-    if (!sums) return TSGEMM_OK;
+    if (!sums || small) return TSGEMM_OK;
     tsg::launch_layer_norm_grad_sum(weight_dtype, part, tsg::layer_norm_grad_groups(dtype, rows, (uint32_t)width),
                                     grad_pitch(width), (uint32_t)width, dgamma, dbeta, s);
     return launched("layer norm gradient sum");

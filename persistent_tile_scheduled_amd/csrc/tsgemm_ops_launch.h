@@ -16,6 +16,7 @@ void launch_layer_norm(int dt, const LnArgs& a, hipStream_t s);
 
 // Workgroups of a layer norm gradient: the count of partial sums per column.
 uint32_t layer_norm_grad_groups(int dt, int64_t rows, uint32_t width);
+bool layer_norm_grad_small(int64_t rows, uint32_t width);  // then no partial sums are left
 void launch_layer_norm_grad(int dt, const LnGradArgs& a, hipStream_t s);
 void launch_layer_norm_grad_sum(int wdt, const float* part, uint32_t groups, uint32_t pitch, uint32_t width, void* dgamma,
                                 void* dbeta, hipStream_t s);

@@ -56,7 +56,10 @@ struct LnGradArgs {
     const float* mean;
     const float* rstd;
     void* dx;
-    float* part;        // [gridDim.x][2][pitch]: a workgroup's sums for dgamma and dbeta; NULL: not wanted
+    float* part;        // [row_groups][2][pitch]: a workgroup's sums for dgamma and dbeta; NULL: not wanted
+    void* dgamma;       // of workgroups past row_groups; NULL: not wanted
+    void* dbeta;
+    uint32_t row_groups;
     int64_t rows, lddy, ldx, lddx;
     uint32_t width, pitch;
     int wdt;
@@ -515,20 +518,67 @@ __global__ __launch_bounds__(1024) void layer_norm_wide_kernel(LnArgs a) {
 // layer norm, gradient: with h = (x - mean) rstd and g = dy gamma,
 //   dx = rstd (g - mean(g) - h mean(g h)),  dgamma = sum_rows dy h,  dbeta = sum_rows dy.
 // A thread keeps its columns' sums over the workgroup's rows in registers; the
-// workgroups' sums meet in a second, small launch in a fixed order.
+// workgroups' sums meet in a second, small launch in a fixed order.  Small
+// matrices are read a second time instead, column by column, by workgroups of
+// the same launch.
 // ---------------------------------------------------------------------------
+template <int WDT>
+__device__ __forceinline__ void store_weight(void* out, uint32_t at, float v) {
+    if (out == nullptr) return;
+    if constexpr (WDT == DT_FP32) ((float*)out)[at] = v;
+    else if constexpr (WDT == DT_BF16) ((__bf16*)out)[at] = (__bf16)v;
+    else ((_Float16*)out)[at] = (_Float16)v;
+}
+
+// dgamma and dbeta of the 8 columns from 8 * block, over all rows; the last ones
+// of a row that is not a multiple of 8 wide reach back as in Chunks.
+template <int DT, bool FULL>
+__device__ __forceinline__ void column_sums(const LnGradArgs& a, uint32_t block) {
+    __shared__ float waves_sums[16][16];
+    constexpr int EB = ElemBytes<DT>::v;
+    const Chunks<1, FULL> c(a.width, block, 1u);
+    float s[16] = {};
+#pragma unroll 4
+    for (int64_t r = threadIdx.x; r < a.rows; r += blockDim.x) {
+        const float mean = a.mean[r], rstd = a.rstd[r];
+        float x[8], d[8];
+        unpack<DT>(load_chunk<DT, FULL>((const char*)a.x + ((size_t)r * a.ldx + c.col[0]) * EB, c.cnt[0]), x);
+        unpack<DT>(load_chunk<DT, FULL>((const char*)a.dy + ((size_t)r * a.lddy + c.col[0]) * EB, c.cnt[0]), d);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            s[e] = __builtin_fmaf(d[e], (x[e] - mean) * rstd, s[e]);
+            s[8 + e] += d[e];
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < 16; ++k) s[k] = group_sum(s[k], 64u);
+    if ((threadIdx.x & 63u) == 0u)
+#pragma unroll
+        for (int k = 0; k < 16; ++k) waves_sums[threadIdx.x >> 6][k] = s[k];
+    lds_barrier();
+    if (threadIdx.x < 16u && (int)(threadIdx.x & 7u) < c.cnt[0]) {
+        float v = 0.f;
+        for (uint32_t w = 0; w < blockDim.x >> 6; ++w) v += waves_sums[w][threadIdx.x];
+        void* out = threadIdx.x < 8u ? a.dgamma : a.dbeta;
+        const uint32_t at = c.col[0] + (threadIdx.x & 7u);
+        if (a.wdt == DT_FP32) store_weight<DT_FP32>(out, at, v);
+        else store_weight<DT>(out, at, v);
+    }
+}
+
 // AHEAD rows are on their way while one is worked on.  With two chunks per
 // thread and row (RAW) a row is kept as it was read and unpacked twice.
 template <int DT, int NC, bool WAVES, bool FULL, int AHEAD>
 __global__ __launch_bounds__(WAVES ? 256 : 1024) void layer_norm_grad_kernel(LnGradArgs a) {
     __shared__ float slots[2][32];
     __shared__ float sums[WAVES ? 256 * 8 : 1];
+    if (blockIdx.x >= a.row_groups) return column_sums<DT, FULL>(a, blockIdx.x - a.row_groups);
     constexpr int EB = ElemBytes<DT>::v;
     constexpr bool RAW = !WAVES && NC > 1;
     const uint32_t T = WAVES ? a.lpr : blockDim.x;
     const uint32_t t = WAVES ? threadIdx.x & (T - 1u) : threadIdx.x;
     const uint32_t rows_wg = WAVES ? 256u / T : 1u;
-    const int64_t step = (int64_t)gridDim.x * rows_wg;
+    const int64_t step = (int64_t)a.row_groups * rows_wg;
     int64_t row = (int64_t)blockIdx.x * rows_wg + (WAVES ? threadIdx.x / T : 0u);
 
     const Chunks<NC, FULL> c(a.width, t, T);
@@ -747,12 +797,7 @@ __global__ __launch_bounds__(1024) void layer_norm_grad_sum_kernel(const float* 
         float v = 0.f;
 #pragma unroll
         for (int w = 0; w < 16; ++w) v += sums[k][w][threadIdx.x & 31u];
-        void* out = k == 0u ? dgamma : dbeta;
-        if (out != nullptr && at < width) {
-            if constexpr (WDT == DT_FP32) ((float*)out)[at] = v;
-            else if constexpr (WDT == DT_BF16) ((__bf16*)out)[at] = (__bf16)v;
-            else ((_Float16*)out)[at] = (_Float16)v;
-        }
+        if (at < width) store_weight<WDT>(k == 0u ? dgamma : dbeta, at, v);
     }
 }
 

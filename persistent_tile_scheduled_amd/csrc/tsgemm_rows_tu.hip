@@ -1,4 +1,6 @@
 // The row operators' kernels and the rules that choose among them.
+#include <cmath>
+
 #include "tsgemm_rows_kernel.h"
 #include "tsgemm_ops_launch.h"
 
@@ -73,14 +75,15 @@ void layer_norm_to(const LnArgs& a, const RowShape& r, hipStream_t s) {
 }
 
 // The gradient reads two matrices, and each workgroup leaves sums of its own:
-// at most three workgroups (65536 x 256 bf16 with 2, 3 and 4: 28.4, 27.5 and
-// 29.7 us).
+// at most three workgroups per compute unit (65536 x 256 bf16 with 2, 3 and 4:
+// 28.4, 27.5 and 29.7 us).
 uint32_t grad_per_cu(const RowShape& r, uint32_t width, int element) { return groups_per_cu(r, width, element, 2u, 3u); }
 
 template <int DT>
 void layer_norm_grad_of(const LnGradArgs& a, const RowShape& r, hipStream_t s) {
     const uint32_t per_cu = grad_per_cu(r, a.width, ElemBytes<DT>::v);
-    const dim3 grid(row_groups(r, a.rows, per_cu)), block(r.threads);
+    const uint32_t columns = a.dgamma || a.dbeta ? (a.width + 7u) / 8u : 0u;
+    const dim3 grid(a.row_groups + columns), block(r.threads);
     if (a.width < 8u) {
         hipLaunchKernelGGL((layer_norm_grad_kernel<DT, 1, true, false, 1>), grid, block, 0, s, a);
         return;
@@ -113,15 +116,35 @@ void launch_layer_norm(int dt, const LnArgs& args, hipStream_t s) {
     else layer_norm_to<DT_FP32>(a, r, s);
 }
 
+// A workgroup more spares the others a row (0.55 us up to 4096 values, then in
+// proportion) and costs its sums' way through memory (16 bytes per column at
+// 3.2 TB/s) and a step of the sums' loop (0.45 us for 128 workgroups): where
+// there are few rows the two meet at the root below.  512 x 4096 bf16 with 1, 3,
+// 4 and 8 rows per workgroup: 16.9, 11.1, 11.1 and 12.4 us; 2000 x 512 with 1, 2
+// and 4 rounds: 10.3, 8.3 and 9.0; 8 x 16384 with 1 and 2: 9.2 and 11.4.
 uint32_t layer_norm_grad_groups(int dt, int64_t rows, uint32_t width) {
     const RowShape r = row_shape(width, true);
-    return row_groups(r, rows, grad_per_cu(r, width, dt == DT_FP32 ? 4 : 2));
+    const uint32_t most = row_groups(r, rows, grad_per_cu(r, width, dt == DT_FP32 ? 4 : 2));
+    const int64_t all = (rows + r.rows - 1) / r.rows;
+    const double sums = 5e-6 * width + 0.0035, row = 0.55 * (width > 4096u ? width / 4096.0 : 1.0);
+    const int64_t rounds = (int64_t)(std::sqrt((double)all * sums / row) + 0.5);
+    return rounds <= 1 ? most : at_most((all + rounds - 1) / rounds, most);
+}
+
+// Whether dgamma and dbeta come from workgroups of the same launch that read the
+// matrices again: 512 x 512 bf16 7.0 -> 3.6 us, 1000 x 1000 10.8 -> 8.5,
+// 1000 x 64 6.0 -> 4.6, and one launch less for the host.  Not for more rows
+// (4000 x 64 6.4 -> 7.3), more values (1000 x 2048 11.2 -> 14.1) or wider ones,
+// whose workgroups have more threads than there are rows (100 x 8000 11 -> 13).
+bool layer_norm_grad_small(int64_t rows, uint32_t width) {
+    return rows <= 1024 && width <= 4096u && rows * (int64_t)width <= 1 << 20;
 }
 
 void launch_layer_norm_grad(int dt, const LnGradArgs& args, hipStream_t s) {
     LnGradArgs a = args;
     const RowShape r = row_shape(a.width, true);
     a.lpr = r.lpr;
+    a.row_groups = layer_norm_grad_groups(dt, a.rows, a.width);
     if (dt == DT_FP16) layer_norm_grad_of<DT_FP16>(a, r, s);
     else if (dt == DT_BF16) layer_norm_grad_of<DT_BF16>(a, r, s);
     else layer_norm_grad_of<DT_FP32>(a, r, s);
