@@ -353,16 +353,18 @@ class Plan:
 
 
 # ---- what a normalised linear layer needs around the MXFP8 product -----------
-# At the smallest shapes a call costs what the host spends on it, so the checks
-# below ask each tensor for each property once and build no message they do not
-# raise.
+# At the smallest shapes a call costs what the host spends on it.  On torch's
+# current stream, with torch's workspaces, the extension module _tsgemm_torch
+# checks the tensors and makes the call; the Python below makes every other call,
+# and says what is wrong with the arguments that the module turned down.
 _FLOATS = {}         # torch dtype -> code, filled on the first call (torch is imported late here)
 _BOOL = None         # torch.bool
 _raw_stream = None   # device index -> handle of torch's current stream
+_short = None        # the extension module that takes a call's tensors whole
 
 
 def _first_call():
-    global _BOOL, _raw_stream
+    global _BOOL, _raw_stream, _short
     import torch
     _BOOL = torch.bool
     _FLOATS.update({torch.float16: FP16, torch.bfloat16: BF16, torch.float32: FP32})
@@ -370,6 +372,25 @@ def _first_call():
     # the Stream object around it (0.1 us instead of 1.8)
     _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
         (lambda index: torch.cuda.current_stream(index).cuda_stream)
+    try:
+        from . import _tsgemm_torch
+    except ImportError as e:
+        raise RuntimeError("the binding's extension module is missing: build it with __graft_entry__.build() "
+                           "(persistent_tile_scheduled_amd._build.build_torch_module())") from e
+    lib = load()
+    _tsgemm_torch.setup(*(ctypes.cast(getattr(lib, "tsgemm_" + name), ctypes.c_void_p).value for name in (
+        "layer_norm", "layer_norm_grad_workspace", "layer_norm_grad", "mx_quantize", "mx_dequantize",
+        "mx_weight_grad_workspace", "mx_weight_grad")), _raw_stream)
+    _short = _tsgemm_torch
+
+
+def _ran(rc) -> bool:
+    """Whether the extension module made the call (None: not with these arguments)."""
+    if rc is None:
+        return False
+    if rc < 0:
+        _check(rc)
+    return True
 
 
 def _dtype_code(name, dtype):
@@ -458,6 +479,11 @@ def layer_norm(x, gamma, beta, eps, y=None, mean=None, rstd=None, codes=None, sc
     (the A and SFA of run_mx; any 1-byte dtype), or both.  gamma and beta (None:
     ones, zeros) are of x's dtype or float32; mean and rstd, float32[rows], are
     given together or not at all."""
+    if stream is None:
+        if _short is None:
+            _first_call()
+        if _ran(_short.layer_norm(x, gamma, beta, eps, y, mean, rstd, codes, scales)):
+            return
     xdt = x.dtype
     dt = _dtype_code("x", xdt)
     rows, width, dev, ldx = _rows_width("x", x)
@@ -484,6 +510,11 @@ def layer_norm_grad(dy, x, gamma, mean, rstd, dx, dgamma=None, dbeta=None, works
     and dx are of x's dtype; gamma (None: ones), dgamma and dbeta share one, x's
     or float32.  `workspace`: a tensor to keep the workgroups' sums in
     (layer_norm_grad_workspace bytes); by default torch's allocator gives one."""
+    if stream is None and workspace is None:
+        if _short is None:
+            _first_call()
+        if _ran(_short.layer_norm_grad(dy, x, gamma, mean, rstd, dx, dgamma, dbeta)):
+            return
     import torch
     xdt, f32 = x.dtype, torch.float32
     dt = _dtype_code("x", xdt)
@@ -514,6 +545,11 @@ def layer_norm_grad_workspace(rows: int, width: int) -> int:
 def mx_quantize(x, codes, scales, stream=None) -> None:
     """tsgemm_mx_quantize: x[rows, width] -> E4M3 codes[rows, width] and E8M0
     scales[rows, width / 32] (any 1-byte dtype), the operands of run_mx."""
+    if stream is None:
+        if _short is None:
+            _first_call()
+        if _ran(_short.mx_quantize(x, codes, scales)):
+            return
     dt = _dtype_code("x", x.dtype)
     rows, width, dev, ldx = _rows_width("x", x)
     pc, ps = _mx(codes, scales, rows, width, dev)
@@ -522,6 +558,11 @@ def mx_quantize(x, codes, scales, stream=None) -> None:
 
 def mx_dequantize(codes, scales, out, stream=None) -> None:
     """tsgemm_mx_dequantize: out[rows, width] = code * scale, rounded once to out's dtype."""
+    if stream is None:
+        if _short is None:
+            _first_call()
+        if _ran(_short.mx_dequantize(out, codes, scales)):
+            return
     dt = _dtype_code("out", out.dtype)
     rows, width, dev, ldo = _rows_width("out", out)
     pc, ps = _mx(codes, scales, rows, width, dev)
@@ -533,6 +574,11 @@ def mx_weight_grad(dy, codes, scales, dw, workspace=None, stream=None) -> None:
     activation (codes, scales).  dy is float16 or bfloat16, dw of dy's dtype or
     float32.  `workspace`: a tensor for the split rows' products
     (mx_weight_grad_workspace bytes); by default torch's allocator gives one."""
+    if stream is None and workspace is None:
+        if _short is None:
+            _first_call()
+        if _ran(_short.mx_weight_grad(dy, codes, scales, dw)):
+            return
     dt, gdt = _dtype_code("dy", dy.dtype), _dtype_code("dw", dw.dtype)
     rows, out, dev, lddy = _rows_width("dy", dy)
     width = dw.shape[-1]

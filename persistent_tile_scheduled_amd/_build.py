@@ -6,6 +6,8 @@ host code (tsgemm.hip), one unit per fp16/bf16 dtype and tile shape
 (tsgemm_mx_tu.hip), and the operators around it: their host code
 (tsgemm_ops.hip), the row operators (tsgemm_rows_tu.hip) and the weight
 gradient (tsgemm_wgrad_tu.hip).  The objects are linked into one shared library.
+Beside it lies the binding's extension module (tsgemm_torch.cpp, g++ and torch's
+headers), which holds no kernel.
 """
 
 from __future__ import annotations
@@ -36,6 +38,31 @@ UNITS = ([("tsgemm.hip", [], "host.o"), ("tsgemm_mx_tu.hip", [], "mx.o"),
           ("tsgemm_wgrad_tu.hip", [], "wgrad.o")] +
          [("tsgemm_gemm_tu.hip", [f"-DTSG_TU_DT={dt}", f"-DTSG_TU_BM={bm}", f"-DTSG_TU_BK={bk}"],
            f"gemm_{dt}_{bm}_{bk}.o") for dt, bm, bk in GEMM_TUS])
+
+
+TORCH_OUT = os.path.join(HERE, "_tsgemm_torch.so")
+
+
+def build_torch_module(out: str = TORCH_OUT) -> str:
+    """Compile the binding's extension module at `out`."""
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = out + ".tmp%d" % os.getpid()
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-I", os.path.join(ROOT, "include"), "-isystem", sysconfig.get_paths()["include"]]
+    for d in cpp_extension.include_paths():
+        cmd += ["-isystem", d]
+    cmd += [os.path.join(CSRC, "tsgemm_torch.cpp"), "-o", tmp, "-L", libs, "-ltorch_python", "-ltorch_cpu", "-lc10",
+            f"-Wl,-rpath,{libs}"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("g++ failed on tsgemm_torch.cpp:\n" + r.stderr[-4000:])
+    os.replace(tmp, out)
+    return out
 
 
 def _jobs() -> int:

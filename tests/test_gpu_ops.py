@@ -591,3 +591,83 @@ def test_mx_norm_linear_step():
     _check(dx, wx, _half(BF16) * wx.abs() + (256 * U + slack) * size, "dx")
     _check(grads["gamma"], wg, (128 * U + slack) * mg, "gamma")
     _check(grads["beta"], wb, (128 * U + slack) * mb, "beta")
+
+
+SMALL_SHAPES = [(1, 8), (2, 9), (1024, 1024), (1025, 1024), (1024, 1025), (1024, 5), (255, 4096), (100, 4097), (65, 63), (1000, 777)]
+
+
+@pytest.mark.parametrize("dtype,wdtype", [(FP16, FP16), (BF16, FP32), (FP32, FP32)], ids=str)
+def test_layer_norm_grad_about_its_borders(dtype, wdtype):
+    """Shapes on both sides of the border between one launch and two, in both
+    ways of calling (torch's workspace and stream, and the caller's): the same
+    bits, within the bound of test_layer_norm_grad."""
+    for rows, width in SMALL_SHAPES:
+        x, dy = _rand(rows, width, dtype, rows + 2 * width), _rand(rows, width, dtype, rows * width + 3, scale=0.05, shift=0.0)
+        gamma, beta = _weights(width, wdtype, seed=width)
+        _, mean, rstd, _ = _norm64(x, gamma, beta, 1e-5)
+        mean, rstd = mean.float(), rstd.float()
+        outs = []
+        for kw in ({}, {"workspace": torch.full((tsg.layer_norm_grad_workspace(rows, width),), 0xFF, dtype=torch.uint8, device=DEV)},
+                   {"stream": torch.cuda.current_stream()}):
+            dx = torch.full_like(x, 7.0)
+            dg, db = (torch.full((width + 16,), 7.0, dtype=wdtype, device=DEV) for _ in range(2))
+            tsg.layer_norm_grad(dy, x, gamma, mean, rstd, dx, dg[:width], db[:width], **kw)
+            outs.append((dx, dg, db))
+            assert (dg[width:] == 7.0).all() and (db[width:] == 7.0).all()
+        for o in outs[1:]:
+            assert all(torch.equal(a, b) for a, b in zip(o, outs[0]))
+        dx, dg, db = outs[0]
+        wx, size, wg, mg, wb, mb = _grad64(dy, x, gamma, mean, rstd)
+        tiny, wtiny = (2.0 ** -25 if t == FP16 else 1e-40 for t in (dtype, wdtype))
+        what = f"{rows}x{width}"
+        _check(dx, wx, _half(dtype) * wx.abs() + 256 * U * size + tiny, what + " dx")
+        _check(dg[:width], wg, _half(wdtype) * wg.abs() + 128 * U * mg + wtiny, what + " dgamma")
+        _check(db[:width], wb, _half(wdtype) * wb.abs() + 128 * U * mb + wtiny, what + " dbeta")
+
+
+def test_both_ways_of_calling_agree():
+    """The extension module (torch's current stream) and the Python marshalling
+    (a stream given) make the same calls."""
+    rows, width, n = 70, 96, 136
+    gamma, beta = _weights(width, BF16, 1)
+    x, dy = _rand(rows, width, BF16, 2), _rand(rows, n, BF16, 3, scale=0.05, shift=0.0)
+    a, b = _outs(rows, width, n, BF16), _outs(rows, width, n, BF16)
+    for o in (a, b):
+        o["dg"], o["db"] = o["dg"].bfloat16(), o["db"].bfloat16()
+    _everything(x, dy, gamma, beta, a)
+    _everything(x, dy, gamma, beta, b, stream=torch.cuda.current_stream())
+    for k in a:
+        assert torch.equal(a[k], b[k]), k
+    with torch.cuda.stream(torch.cuda.Stream()):
+        c = _outs(rows, width, n, BF16)
+        c["dg"], c["db"] = c["dg"].bfloat16(), c["db"].bfloat16()
+        torch.cuda.current_stream().wait_stream(torch.cuda.default_stream())
+        _everything(x, dy, gamma, beta, c)
+        torch.cuda.current_stream().synchronize()
+    for k in a:
+        assert torch.equal(a[k], c[k]), k
+
+
+def test_bad_tensors_are_named():
+    x, v = _rand(4, 64, BF16, 1), torch.ones(64, device=DEV)
+    codes, scales = _held(4, 64)
+    with pytest.raises(ValueError, match="gamma"):
+        tsg.layer_norm(x, v[:32], v, 1e-5, y=torch.empty_like(x))
+    with pytest.raises(ValueError, match="y must be"):
+        tsg.layer_norm(x, v, v, 1e-5, y=torch.empty((4, 63), dtype=BF16, device=DEV))
+    with pytest.raises(ValueError, match="beta"):
+        tsg.layer_norm(x, v, v.bfloat16(), 1e-5, y=torch.empty_like(x))
+    with pytest.raises(ValueError, match="contiguous rows"):
+        tsg.mx_quantize(x.t(), codes, scales)
+    with pytest.raises(ValueError, match="scales"):
+        tsg.mx_quantize(x, codes, scales[:, :1])
+    with pytest.raises(ValueError, match="codes"):
+        tsg.mx_dequantize(codes.bool(), scales, x)
+    with pytest.raises(ValueError, match="divisible by 32"):
+        tsg.mx_quantize(x[:, :40], codes, scales)
+    with pytest.raises(ValueError, match="dw"):
+        tsg.mx_weight_grad(x, codes, scales, torch.empty((63, 64), device=DEV))
+    with pytest.raises(tsg.TsgemmError, match="no output"):
+        tsg.layer_norm(x, v, v, 1e-5)
+    with pytest.raises(tsg.TsgemmError, match="divisible by 8"):
+        tsg.mx_weight_grad(_rand(4, 60, BF16, 1), codes, scales, torch.empty((60, 64), device=DEV))

@@ -172,3 +172,22 @@ def test_binding_refuses_host_tensors_and_shapes():
         tsg.mx_weight_grad(x, None, None, torch.zeros((64, 64)))
     with pytest.raises(ValueError, match="float16, bfloat16 or float32"):
         tsg.layer_norm(x.double(), v, v, 1e-5, y=x)
+
+
+def test_extension_module_turns_down_what_the_binding_explains():
+    """What the module does not take it leaves to the Python checks: None, no
+    exception and no call."""
+    with pytest.raises(ValueError):
+        tsg.mx_quantize(torch.zeros((4, 64)), None, None)     # loads the module
+    short = tsg._short
+    x, v, b = torch.zeros((4, 64)), torch.zeros(64), torch.zeros((4, 64), dtype=torch.uint8)
+    assert short.layer_norm(x, v, v, 1e-5, x, None, None, None, None) is None
+    assert short.layer_norm(x, v, v) is None
+    assert short.layer_norm(3, v, v, 1e-5, x, None, None, None, None) is None
+    assert short.layer_norm_grad(x, x, v, v, v, x, None, None) is None
+    assert short.mx_quantize(x, b, b) is None
+    assert short.mx_quantize(None, None, None) is None
+    assert short.mx_dequantize(x, b, b) is None
+    assert short.mx_weight_grad(x, b, b, x) is None
+    with pytest.raises(TypeError):
+        short.setup(1, 2)
