@@ -261,7 +261,8 @@ int tsgemm_run_mx_noalloc(const tsgemm_plan* plan, const void* A, const void* SF
  * SFA of tsgemm_run_mx: codes uint8[rows][width] (16-byte aligned), scales
  * uint8[rows][width/32] (4-byte aligned), width % 32 == 0.  All pointers are
  * DEVICE pointers owned by the caller, outputs must not overlap inputs, and
- * every call only enqueues work on `stream`.  Sums and statistics are fp32;
+ * every call only enqueues work on `stream`.  Sums and statistics are fp32 (layer
+ * norm's cross lanes in fp64);
  * a result is rounded once, to nearest, ties to even.
  *
  * tsgemm_layer_norm: for every row of x
@@ -271,7 +272,8 @@ int tsgemm_run_mx_noalloc(const tsgemm_plan* plan, const void* A, const void* SF
  *   beta (NULL: ones, zeros) of `weight_dtype`, which is dtype or TSGEMM_FP32.
  *   Outputs: y, or codes and scales (y held as MX, without a rounding to dtype
  *   before), or both; mean and rstd (fp32[rows]) together or not at all.
- *   width >= 1; eps finite, >= 0; rows == 0 launches nothing. */
+ *   width >= 1; eps finite, >= 0; rows == 0 launches nothing.  A row whose sum
+ *   or squares pass fp32's range has no finite statistics. */
 int tsgemm_layer_norm(int64_t rows, int64_t width, int dtype, int weight_dtype, const void* x, int64_t ldx,
                       const void* gamma, const void* beta, float eps, void* y, int64_t ldy, float* mean,
                       float* rstd, void* codes, void* scales, void* stream);

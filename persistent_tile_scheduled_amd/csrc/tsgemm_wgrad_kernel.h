@@ -81,7 +81,7 @@ __device__ __forceinline__ void split_f16(i16x8 v, i16x8& hi, i16x8& lo) {
     for (int e = 0; e < 8; ++e) {
         const float f = (float)x[e] * (float)(1 << kShift);
         h[e] = (__bf16)f;
-        l[e] = (__bf16)(f - (float)h[e]);
+        l[e] = __builtin_isinf(f) ? (__bf16)0.f : (__bf16)(f - (float)h[e]);  // inf - inf is no number
     }
     hi = __builtin_bit_cast(i16x8, h);
     lo = __builtin_bit_cast(i16x8, l);

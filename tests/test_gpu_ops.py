@@ -395,6 +395,25 @@ def test_weight_grad_fp16_keeps_far_scales(rows, out, width):
         _check(dw, want, (2 * rows + 64) * U * mag + U * want.abs(), f"part {part}")
 
 
+def test_weight_grad_fp16_infinite_dy():
+    """An infinite dy makes its row of dw infinite, with the sign of the codes, in
+    slabs of ordinary and of far scales alike; the other rows stay."""
+    rows, out, width = 130, 72, 96
+    codes = torch.full((rows, width), 0x38, dtype=torch.uint8, device=DEV)      # 1
+    codes[:, 1::2] = 0xB8                                                        # -1
+    dy = _rand(rows, out, FP16, 7, scale=0.05, shift=0.0)
+    for field in (127, 127 + 60):
+        scales = torch.full((rows, width // 32), field, dtype=torch.uint8, device=DEV)
+        base, odd = torch.empty((out, width), device=DEV), torch.empty((out, width), device=DEV)
+        tsg.mx_weight_grad(dy, codes, scales, base)
+        z = dy.clone()
+        z[77, 13] = float("inf")
+        tsg.mx_weight_grad(z, codes, scales, odd)
+        assert (odd[13, 0::2] == float("inf")).all() and (odd[13, 1::2] == -float("inf")).all(), field
+        keep = [i for i in range(out) if i != 13]
+        assert torch.equal(odd[keep], base[keep])
+
+
 def test_weight_grad_empty_and_odd_values():
     dw = torch.full((64, 96), 7.0, device=DEV)
     tsg.mx_weight_grad(torch.empty((0, 64), dtype=BF16, device=DEV), torch.empty((0, 96), dtype=torch.uint8, device=DEV),
