@@ -538,7 +538,7 @@ __device__ __forceinline__ void column_sums(const LnGradArgs& a, uint32_t block)
     constexpr int EB = ElemBytes<DT>::v;
     const Chunks<1, FULL> c(a.width, block, 1u);
     float s[16] = {};
-#pragma unroll 4
+#pragma unroll 2
     for (int64_t r = threadIdx.x; r < a.rows; r += blockDim.x) {
         const float mean = a.mean[r], rstd = a.rstd[r];
         float x[8], d[8];
@@ -743,14 +743,29 @@ __global__ __launch_bounds__(1024) void layer_norm_grad_wide_kernel(LnGradArgs a
             load_weights<DT>(a.gamma, a.wdt, col, cnt, 1.f, gam);
             float o[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                h[e] = e < cnt ? (h[e] - mean) * rstd : 0.f;
-                if (i < rounds) {
-                    if (part != nullptr && e < cnt) {
-                        float* p = part + col + e;
-                        p[0] = first ? g[e] * h[e] : __builtin_fmaf(g[e], h[e], p[0]);
-                        p[a.pitch] = first ? g[e] : p[a.pitch] + g[e];
+            for (int e = 0; e < 8; ++e) h[e] = e < cnt ? (h[e] - mean) * rstd : 0.f;
+            if (part != nullptr && i < rounds) {  // the pitch is a multiple of 8: a cut chunk has room for 8
+                f32x4* p = (f32x4*)(part + col);
+                f32x4* q = (f32x4*)(part + a.pitch + col);
+#pragma unroll
+                for (int w = 0; w < 2; ++w) {
+                    f32x4 sg = {0.f, 0.f, 0.f, 0.f}, sb = sg;
+                    if (!first) {
+                        sg = p[w];
+                        sb = q[w];
                     }
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        sg[e] = __builtin_fmaf(g[4 * w + e], h[4 * w + e], sg[e]);
+                        sb[e] += g[4 * w + e];
+                    }
+                    p[w] = sg;
+                    q[w] = sb;
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                if (i < rounds) {
                     g[e] *= gam[e];
                     s[0] += g[e];
                     s[1] = __builtin_fmaf(g[e], h[e], s[1]);
