@@ -262,8 +262,8 @@ int tsgemm_run_mx_noalloc(const tsgemm_plan* plan, const void* A, const void* SF
  * uint8[rows][width/32] (4-byte aligned), width % 32 == 0.  All pointers are
  * DEVICE pointers owned by the caller, outputs must not overlap inputs, and
  * every call only enqueues work on `stream`.  Sums and statistics are fp32 (layer
- * norm's cross lanes in fp64);
- * a result is rounded once, to nearest, ties to even.
+ * norm's cross lanes in fp64); a result is rounded once, to nearest, ties to
+ * even.
  *
  * tsgemm_layer_norm: for every row of x
  *     mean = sum(x) / width      rstd = (sum((x - mean)^2) / width + eps)^(-1/2)

@@ -6,6 +6,12 @@
 // in registers in fp32 and written once.  Statistics, sums and gradients of the
 // weights are fp32; a value is rounded once, when it is stored.
 //
+// Measured on the MI355X against a copy's 5.35 TB/s (inputs and outputs changing
+// from pass to pass): layer norm 16000 x 4000 fp16 48.6 us, 5.27 TB/s; 8192 x 8192
+// bf16 to codes 44 us, 4.6 TB/s, of which its vector instructions alone take 29;
+// gradient 8192 x 8192 bf16 81 us, 4.97 TB/s (17 MB of partial sums come on top);
+// quantize 16384 x 4096 bf16 36.9 us and dequantize 8192 x 8192 36.5 us, 5.5 TB/s.
+//
 // Everything works on chunks of 8 consecutive values of a row (16 bytes of a
 // 16-bit type): four neighbouring lanes hold an MX block of 32, whose largest
 // magnitude is a matter of two cross-lane moves inside the quad.  Rows need
@@ -467,7 +473,8 @@ __global__ __launch_bounds__(WAVES ? 256 : 1024) void layer_norm_kernel(LnArgs a
 }
 
 // Rows of any width, one workgroup of 1024 threads each: the row is read three
-// times (the second and third time mostly out of a cache).
+// times (the second and third time mostly out of a cache).  Only past 16384
+// values, which no longer fit the registers: 2000 x 30016 bf16 95 us, 2.5 TB/s.
 template <int DT, bool CODES>
 __global__ __launch_bounds__(1024) void layer_norm_wide_kernel(LnArgs a) {
     __shared__ double slots[2][16];
@@ -714,7 +721,8 @@ __global__ __launch_bounds__(WAVES ? 256 : 1024) void layer_norm_grad_kernel(LnG
 }
 
 // Rows of any width, one workgroup of 1024 threads each; the workgroup's sums
-// for the weights gather in its own part of the workspace.
+// for the weights gather in its own part of the workspace, 32 bytes of which move
+// for every value: 2000 x 30016 bf16 306 us (value by value 553).
 template <int DT>
 __global__ __launch_bounds__(1024) void layer_norm_grad_wide_kernel(LnGradArgs a) {
     __shared__ float slots[2][32];
@@ -817,7 +825,8 @@ __global__ __launch_bounds__(1024) void layer_norm_grad_sum_kernel(const float* 
 }
 
 // ---------------------------------------------------------------------------
-// activations to MX and back, 8 values per thread
+// activations to MX and back, 8 values per thread: bound by memory at any size
+// that fills the chip, by the launch (2.1 us for 512 x 512) below
 // ---------------------------------------------------------------------------
 // Chunk i of the matrix -> its row and column.  `cpr` chunks per row.
 struct ChunkAt { int64_t row; uint32_t col; };
