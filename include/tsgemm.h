@@ -261,8 +261,8 @@ int tsgemm_run_mx_noalloc(const tsgemm_plan* plan, const void* A, const void* SF
  * SFA of tsgemm_run_mx: codes uint8[rows][width] (16-byte aligned), scales
  * uint8[rows][width/32] (4-byte aligned), width % 32 == 0.  All pointers are
  * DEVICE pointers owned by the caller, outputs must not overlap inputs, and
- * every call only enqueues work on `stream`.  Sums and statistics are fp32 (layer
- * norm's cross lanes in fp64); a result is rounded once, to nearest, ties to
+ * every call only enqueues work on `stream`.  Sums and statistics are fp32
+ * (layer norm's join in fp64); a result is rounded once, to nearest, ties to
  * even.
  *
  * tsgemm_layer_norm: for every row of x

@@ -219,8 +219,8 @@ __device__ __forceinline__ float group_sum(float v, uint32_t lanes) {
     return v;
 }
 
-// The same in fp64, for the forward statistics: a thread's own few values add up
-// in fp32, what crosses lanes in fp64.
+// The same in fp64, for the forward statistics of rows that lanes of one wave
+// hold: a thread's own few values add up in fp32, what crosses lanes in fp64.
 template <int CTRL>
 __device__ __forceinline__ double dpp(double v) {
     const u32x2 b = __builtin_bit_cast(u32x2, v);
@@ -248,8 +248,8 @@ __device__ __forceinline__ double group_sum(double v, uint32_t lanes) {
     return v;
 }
 
-// Sum over the workgroup's waves of K values each.  `slot`: 16 * K values of
-// LDS, another than the previous call's (one barrier per call then suffices: a
+// Sum over the workgroup of K values each: over a wave in fp32, over the waves
+// in F.  `slot`: 16 * K values of LDS, another than the previous call's (one barrier per call then suffices: a
 // wave reaches the next call's barrier only after it has read this call's slot).
 template <int K, class F>
 __device__ __forceinline__ void block_sum(F (&v)[K], F* slot) {
