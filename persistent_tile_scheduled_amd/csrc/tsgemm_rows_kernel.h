@@ -249,8 +249,9 @@ __device__ __forceinline__ double group_sum(double v, uint32_t lanes) {
 }
 
 // Sum over the workgroup of K values each: over a wave in fp32, over the waves
-// in F.  `slot`: 16 * K values of LDS, another than the previous call's (one barrier per call then suffices: a
-// wave reaches the next call's barrier only after it has read this call's slot).
+// in F.  `slot`: 16 * K values of LDS, another than the previous call's (one
+// barrier per call then suffices: a wave reaches the next call's barrier only
+// after it has read this call's slot).
 template <int K, class F>
 __device__ __forceinline__ void block_sum(F (&v)[K], F* slot) {
     const uint32_t wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
