@@ -109,7 +109,14 @@ __global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void wgrad_kernel(WgradArgs
     const uint32_t lds_base = (uint32_t)reinterpret_cast<uintptr_t>((lds_u8*)smem);
     const uint32_t lane = threadIdx.x & 63u;
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    uint32_t stress_ctr = 0;  // race-detection build only (TSG_STRESS)
+    // Race-detection build only (TSG_STRESS), and not for fp16: its two pipelines
+    // with a branch at every pause leave the compiler too few accumulators, which
+    // it then copies right beside the MFMAs in asm that it cannot see to wait for.
+    // What bf16's pipeline waits for, fp16's does too.
+    uint32_t stress_ctr = 0;
+    auto pause = [&](auto site_c) __attribute__((always_inline)) {
+        if constexpr (DT == DT_BF16) stress_pause<decltype(site_c)::value>(wave, stress_ctr);
+    };
     const uint32_t wr = wave >> 1, wc = wave & 1u;
     const uint32_t out = args.out, width = args.width, w32 = width / 32u;
 
@@ -170,7 +177,7 @@ __global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void wgrad_kernel(WgradArgs
     }
     auto dma = [&](auto q_c, auto s_c) __attribute__((always_inline)) {
         constexpr int q = decltype(q_c)::value, S = decltype(s_c)::value;
-        stress_pause<2>(wave, stress_ctr);
+        pause(std::integral_constant<int, 2>{});
         dma16_at<(uint32_t)(S * T::A_STAGE + q * 1024)>(lds_base + wave * NA * 1024u, a_voff[q], rs_a);
     };
 
@@ -347,11 +354,11 @@ __global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void wgrad_kernel(WgradArgs
     auto period = [&](auto mode_c, auto s_c, uint32_t next, uint32_t& end) __attribute__((always_inline)) {
         constexpr int MODE = decltype(mode_c)::value, S = decltype(s_c)::value;
         using OTHER = std::integral_constant<int, 1 - S>;
-        stress_pause<0>(wave, stress_ctr);
+        pause(std::integral_constant<int, 0>{});
         wait_vm<0>();    // the next slab's dy and the codes after it have landed
         if constexpr (MODE == WG_FP16) put_flag(s_c);
         lds_barrier();   // ... for every wave; stage S is read out, its successor written
-        stress_pause<1>(wave, stress_ctr);
+        pause(std::integral_constant<int, 1>{});
         next_a();
         next_c();
         kstep(mode_c, I1{}, [&](auto g_c) __attribute__((always_inline)) {
