@@ -299,7 +299,14 @@ __global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void wgrad_kernel(WgradArgs
 #pragma unroll
     for (int fm = 0; fm < FM; ++fm)
 #pragma unroll
-        for (int fn = 0; fn < FN; ++fn) acc[fm][fn] = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int fn = 0; fn < FN; ++fn) {
+            acc[fm][fn] = f32x4{0.f, 0.f, 0.f, 0.f};
+            asm volatile("" : "+a"(acc[fm][fn]));  // cleared here, in registers of its own
+        }
+    // A vector write of a register -> an MFMA that reads it: two wait states.  The
+    // MFMAs are asm, before which the compiler places none; left to itself it
+    // cleared each accumulator right in front of its first MFMA.
+    asm volatile("s_nop 1" ::: "memory");
 
     // One 32-row k-step on set K: FM * FN MFMAs, rows of blocks in order, the
     // columns there and back.  `between(s)` issues what goes after MFMA s.
