@@ -27,6 +27,9 @@
  *     code and then sets a message readable with tsgemm_last_error();
  *   - pointer arguments named A, B, C are DEVICE pointers, the caller owns
  *     them; `out` arguments of the schedule calls are HOST pointers;
+ *   - work is launched on the current HIP device, to which `stream` and the
+ *     DEVICE pointers have to belong (the Python binding makes the tensors'
+ *     device current for its calls);
  *   - the library keeps no pointer after a call returns; a plan is immutable
  *     once configured (create + the set_* calls), so concurrent runs of one
  *     plan on different streams are safe.

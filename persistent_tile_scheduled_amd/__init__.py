@@ -165,6 +165,25 @@ def _check(rc: int) -> int:
     return rc
 
 
+def _enqueue(call, stream, first, *others) -> None:
+    """call(handle of `stream`, or of torch's current one) with the tensors' device
+    current: the library launches on the current device."""
+    import torch
+    dev = first.get_device()
+    for t in others:
+        if t.get_device() != dev:
+            raise ValueError(f"the tensors of a call must be on one device, got CUDA devices {dev} and {t.get_device()}")
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    elif stream.device_index != dev:
+        raise ValueError(f"the stream is of CUDA device {stream.device_index}, the tensors are on device {dev}")
+    if torch.cuda.current_device() == dev:
+        _check(call(stream.cuda_stream))
+    else:
+        with torch.cuda.device(dev):
+            _check(call(stream.cuda_stream))
+
+
 _DTYPES = {"fp16": FP16, "bf16": BF16, "mxfp8": MXFP8, FP16: FP16, BF16: BF16, MXFP8: MXFP8}
 
 
@@ -246,6 +265,9 @@ class Plan:
         import torch
         if trace.dtype != torch.int32 or not trace.is_cuda or not trace.is_contiguous():
             raise ValueError("trace must be a contiguous int32 CUDA tensor")
+
+    def _trace_pointer(self, trace):
+        """... that holds what a run on the current device may write."""
         need = 4 * self.trace_rows()
         if trace.numel() < need:
             raise ValueError(f"trace holds {trace.numel()} int32, the run may write {need}")
@@ -264,17 +286,13 @@ class Plan:
 
     def run(self, A, B, C, stream=None) -> None:
         """C = A @ B on `stream` (a torch.cuda.Stream; default: torch's current stream)."""
-        import torch
         a, b, c = self._args(A, B, C)
-        s = (stream or torch.cuda.current_stream(C.device)).cuda_stream
-        _check(self._lib.tsgemm_run(self._h, a, b, c, s))
+        _enqueue(lambda s: self._lib.tsgemm_run(self._h, a, b, c, s), stream, C, A, B)
 
     def run_traced(self, A, B, C, trace, stream=None) -> None:
-        import torch
         a, b, c = self._args(A, B, C)
-        t = self._check_trace(trace)
-        s = (stream or torch.cuda.current_stream(C.device)).cuda_stream
-        _check(self._lib.tsgemm_run_traced(self._h, a, b, c, s, t))
+        self._check_trace(trace)
+        _enqueue(lambda s: self._lib.tsgemm_run_traced(self._h, a, b, c, s, self._trace_pointer(trace)), stream, C, A, B, trace)
 
     def _mx_args(self, A, SFA, B, SFB, C):
         import torch
@@ -295,18 +313,14 @@ class Plan:
     def run_mx(self, A, SFA, B, SFB, C, stream=None) -> None:
         """Block-scaled FP8 product (tsgemm_run_mx): A[M,K], B[N,K] E4M3 codes,
         SFA[M,K/32], SFB[N,K/32] E8M0 codes (any 1-byte dtype), C[M,N] bf16."""
-        import torch
         a, sa, b, sb, c = self._mx_args(A, SFA, B, SFB, C)
-        s = (stream or torch.cuda.current_stream(C.device)).cuda_stream
-        _check(self._lib.tsgemm_run_mx(self._h, a, sa, b, sb, c, s))
+        _enqueue(lambda s: self._lib.tsgemm_run_mx(self._h, a, sa, b, sb, c, s), stream, C, A, SFA, B, SFB)
 
     def run_mx_noalloc(self, A, SFA, B, SFB, C, stream=None) -> None:
         """tsgemm_run_mx_noalloc: run_mx through the packed-scale kernel with the
         packed scales in the library's static workspace (allocates nothing)."""
-        import torch
         a, sa, b, sb, c = self._mx_args(A, SFA, B, SFB, C)
-        s = (stream or torch.cuda.current_stream(C.device)).cuda_stream
-        _check(self._lib.tsgemm_run_mx_noalloc(self._h, a, sa, b, sb, c, s))
+        _enqueue(lambda s: self._lib.tsgemm_run_mx_noalloc(self._h, a, sa, b, sb, c, s), stream, C, A, SFA, B, SFB)
 
     def mx_packed_scale_bytes(self, operand: int) -> int:
         """Bytes of the packed scale array of operand 0 (SFA) or 1 (SFB)."""
@@ -315,7 +329,6 @@ class Plan:
     def mx_pack_scales(self, SF, SFP, operand: int, stream=None) -> None:
         """tsgemm_mx_pack_scales: SF [rows, K/32] (1-byte, CUDA) -> SFP (1-byte CUDA tensor of
         mx_packed_scale_bytes(operand) bytes)."""
-        import torch
         rows = self.M if operand == 0 else self.N
         if SF.element_size() != 1 or tuple(SF.shape) != (rows, self.K // 32) or not SF.is_contiguous() \
                 or not SF.is_cuda:
@@ -323,8 +336,8 @@ class Plan:
         need = self.mx_packed_scale_bytes(operand)
         if SFP.element_size() != 1 or SFP.numel() != need or not SFP.is_contiguous() or not SFP.is_cuda:
             raise ValueError(f"SFP must be a contiguous 1-byte CUDA tensor of {need} bytes")
-        s = (stream or torch.cuda.current_stream(SFP.device)).cuda_stream
-        _check(self._lib.tsgemm_mx_pack_scales(self._h, operand, SF.data_ptr(), SFP.data_ptr(), s))
+        _enqueue(lambda s: self._lib.tsgemm_mx_pack_scales(self._h, operand, SF.data_ptr(), SFP.data_ptr(), s),
+                 stream, SFP, SF)
 
     def run_mx_packed(self, A, SFAP, B, SFBP, C, stream=None) -> None:
         """tsgemm_run_mx_packed: as run_mx with scales from mx_pack_scales."""
@@ -340,38 +353,37 @@ class Plan:
                 raise ValueError(f"{name} must be a contiguous 1-byte CUDA tensor of {need} bytes")
         if C.dtype != torch.bfloat16 or tuple(C.shape) != (self.M, self.N) or not C.is_contiguous() or not C.is_cuda:
             raise ValueError(f"C must be a contiguous torch.bfloat16 CUDA tensor of shape {(self.M, self.N)}")
-        s = (stream or torch.cuda.current_stream(C.device)).cuda_stream
-        _check(self._lib.tsgemm_run_mx_packed(self._h, A.data_ptr(), SFAP.data_ptr(), B.data_ptr(),
-                                              SFBP.data_ptr(), C.data_ptr(), s))
+        _enqueue(lambda s: self._lib.tsgemm_run_mx_packed(self._h, A.data_ptr(), SFAP.data_ptr(), B.data_ptr(), SFBP.data_ptr(),
+                                                          C.data_ptr(), s), stream, C, A, SFAP, B, SFBP)
 
     def run_mx_traced(self, A, SFA, B, SFB, C, trace, stream=None) -> None:
-        import torch
         a, sa, b, sb, c = self._mx_args(A, SFA, B, SFB, C)
-        t = self._check_trace(trace)
-        s = (stream or torch.cuda.current_stream(C.device)).cuda_stream
-        _check(self._lib.tsgemm_run_mx_traced(self._h, a, sa, b, sb, c, s, t))
+        self._check_trace(trace)
+        _enqueue(lambda s: self._lib.tsgemm_run_mx_traced(self._h, a, sa, b, sb, c, s, self._trace_pointer(trace)),
+                 stream, C, A, SFA, B, SFB, trace)
 
 
 # ---- what a normalised linear layer needs around the MXFP8 product -----------
 # At the smallest shapes a call costs what the host spends on it.  On torch's
-# current stream, with torch's workspaces, the extension module _tsgemm_torch
-# checks the tensors and makes the call; the Python below makes every other call,
-# and says what is wrong with the arguments that the module turned down.
+# current device and stream, with torch's workspaces, the extension module
+# _tsgemm_torch checks the tensors and makes the call; the Python below makes every
+# other call, and says what is wrong with the arguments that the module turned down.
 _FLOATS = {}         # torch dtype -> code, filled on the first call (torch is imported late here)
 _BOOL = None         # torch.bool
-_raw_stream = None   # device index -> handle of torch's current stream
 _short = None        # the extension module that takes a call's tensors whole
 
 
 def _first_call():
-    global _BOOL, _raw_stream, _short
+    global _BOOL, _short
     import torch
     _BOOL = torch.bool
     _FLOATS.update({torch.float16: FP16, torch.bfloat16: BF16, torch.float32: FP32})
     # the same handle as torch.cuda.current_stream(device).cuda_stream without
-    # the Stream object around it (0.1 us instead of 1.8)
-    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    # the Stream object around it (0.1 us instead of 1.8), and the current device
+    # without the question whether torch has begun to use GPUs
+    raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
         (lambda index: torch.cuda.current_stream(index).cuda_stream)
+    device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
     try:
         from . import _tsgemm_torch
     except ImportError as e:
@@ -380,7 +392,7 @@ def _first_call():
     lib = load()
     _tsgemm_torch.setup(*(ctypes.cast(getattr(lib, "tsgemm_" + name), ctypes.c_void_p).value for name in (
         "layer_norm", "layer_norm_grad_workspace", "layer_norm_grad", "mx_quantize", "mx_dequantize",
-        "mx_weight_grad_workspace", "mx_weight_grad")), _raw_stream)
+        "mx_weight_grad_workspace", "mx_weight_grad")), raw_stream, device)
     _short = _tsgemm_torch
 
 
@@ -451,10 +463,6 @@ def _mx(codes, scales, rows, width, dev):
     return codes.data_ptr(), scales.data_ptr()
 
 
-def _stream_of(dev, stream):
-    return _raw_stream(dev) if stream is None else stream.cuda_stream
-
-
 def _workspace(nbytes, workspace, like, stream):
     """Pointer, size and tensor of a workspace: the caller's, or one of torch's
     allocator, taken for the stream that the kernels run on."""
@@ -500,8 +508,8 @@ def layer_norm(x, gamma, beta, eps, y=None, mean=None, rstd=None, codes=None, sc
         pr = _vector("rstd", rstd, rows, torch.float32, dev)
     if codes is not None or scales is not None:
         pc, ps = _mx(codes, scales, rows, width, dev)
-    _check(load().tsgemm_layer_norm(rows, width, dt, wdt, x.data_ptr(), ldx, pg, pb, eps, py, ldy, pm, pr, pc, ps,
-                                    _stream_of(dev, stream)))
+    _enqueue(lambda s: load().tsgemm_layer_norm(rows, width, dt, wdt, x.data_ptr(), ldx, pg, pb, eps, py, ldy, pm, pr, pc, ps, s),
+             stream, x)
 
 
 def layer_norm_grad(dy, x, gamma, mean, rstd, dx, dgamma=None, dbeta=None, workspace=None, stream=None) -> None:
@@ -533,8 +541,8 @@ def layer_norm_grad(dy, x, gamma, mean, rstd, dx, dgamma=None, dbeta=None, works
     pr = _vector("rstd", rstd, rows, f32, dev)
     need = 0 if pdg is None and pdb is None else layer_norm_grad_workspace(rows, width)
     pw, have, keep = _workspace(need, workspace, x, stream)
-    _check(load().tsgemm_layer_norm_grad(rows, width, dt, wdt, pdy, lddy, x.data_ptr(), ldx, pg, pm, pr, pdx, lddx, pdg,
-                                         pdb, pw, have, _stream_of(dev, stream)))
+    _enqueue(lambda s: load().tsgemm_layer_norm_grad(rows, width, dt, wdt, pdy, lddy, x.data_ptr(), ldx, pg, pm, pr, pdx, lddx,
+                                                     pdg, pdb, pw, have, s), stream, x)
 
 
 def layer_norm_grad_workspace(rows: int, width: int) -> int:
@@ -553,7 +561,7 @@ def mx_quantize(x, codes, scales, stream=None) -> None:
     dt = _dtype_code("x", x.dtype)
     rows, width, dev, ldx = _rows_width("x", x)
     pc, ps = _mx(codes, scales, rows, width, dev)
-    _check(load().tsgemm_mx_quantize(rows, width, dt, x.data_ptr(), ldx, pc, ps, _stream_of(dev, stream)))
+    _enqueue(lambda s: load().tsgemm_mx_quantize(rows, width, dt, x.data_ptr(), ldx, pc, ps, s), stream, x)
 
 
 def mx_dequantize(codes, scales, out, stream=None) -> None:
@@ -566,7 +574,7 @@ def mx_dequantize(codes, scales, out, stream=None) -> None:
     dt = _dtype_code("out", out.dtype)
     rows, width, dev, ldo = _rows_width("out", out)
     pc, ps = _mx(codes, scales, rows, width, dev)
-    _check(load().tsgemm_mx_dequantize(rows, width, dt, pc, ps, out.data_ptr(), ldo, _stream_of(dev, stream)))
+    _enqueue(lambda s: load().tsgemm_mx_dequantize(rows, width, dt, pc, ps, out.data_ptr(), ldo, s), stream, out)
 
 
 def mx_weight_grad(dy, codes, scales, dw, workspace=None, stream=None) -> None:
@@ -586,8 +594,8 @@ def mx_weight_grad(dy, codes, scales, dw, workspace=None, stream=None) -> None:
         raise ValueError(f"dw must be a contiguous tensor of shape {(out, width)} on CUDA device {dev}")
     pc, ps = _mx(codes, scales, rows, width, dev)
     pw, have, keep = _workspace(mx_weight_grad_workspace(rows, out, width), workspace, dy, stream)
-    _check(load().tsgemm_mx_weight_grad(rows, out, width, dt, gdt, dy.data_ptr(), lddy, pc, ps, dw.data_ptr(), pw, have,
-                                        _stream_of(dev, stream)))
+    _enqueue(lambda s: load().tsgemm_mx_weight_grad(rows, out, width, dt, gdt, dy.data_ptr(), lddy, pc, ps, dw.data_ptr(), pw,
+                                                    have, s), stream, dy)
 
 
 def mx_weight_grad_workspace(rows: int, out: int, width: int) -> int:

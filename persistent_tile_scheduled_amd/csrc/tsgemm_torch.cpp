@@ -5,9 +5,10 @@
 // 4.0).
 //
 // Every function takes its Python namesake's tensors and scalars in order,
-// workspace excluded, for torch's current stream.  It returns the C entry's code,
-// or None, with nothing done, for arguments that are not exactly as the Python
-// function wants them; that one then says what is wrong with them.
+// workspace excluded, for tensors on torch's current device and its current
+// stream.  It returns the C entry's code, or None, with nothing done, for
+// arguments that are not exactly as the Python function wants them or on another
+// device; that one then makes their device current or says what is wrong with them.
 #include <Python.h>
 
 #include <torch/csrc/autograd/python_variable.h>
@@ -26,7 +27,8 @@ decltype(&tsgemm_mx_quantize) p_mx_quantize;
 decltype(&tsgemm_mx_dequantize) p_mx_dequantize;
 decltype(&tsgemm_mx_weight_grad_workspace) p_mx_weight_grad_workspace;
 decltype(&tsgemm_mx_weight_grad) p_mx_weight_grad;
-PyObject* raw_stream;  // device index -> handle of torch's current stream
+PyObject* raw_stream;      // device index -> handle of torch's current stream
+PyObject* current_device;  // -> device index, on which the C entries launch
 
 int code_of(at::ScalarType t) {
     return t == at::kHalf ? TSGEMM_FP16 : t == at::kBFloat16 ? TSGEMM_BF16 : t == at::kFloat ? TSGEMM_FP32 : 0;
@@ -105,7 +107,16 @@ struct Args {
         }
         return t->data_ptr();
     }
+    // the stream to launch on, of the tensors' device, which has to be the current one
     void* stream() {
+        PyObject* now = PyObject_CallNoArgs(current_device);
+        const long here = now ? PyLong_AsLong(now) : -1;
+        Py_XDECREF(now);
+        if (here != dev) {
+            PyErr_Clear();
+            ok = false;
+            return nullptr;
+        }
         PyObject* d = PyLong_FromLong(dev);
         PyObject* h = d ? PyObject_CallOneArg(raw_stream, d) : nullptr;
         Py_XDECREF(d);
@@ -145,8 +156,8 @@ PyObject* guarded(F&& f) {
 }
 
 PyObject* setup(PyObject*, PyObject* const* a, Py_ssize_t n) {
-    if (n != 8) {
-        PyErr_SetString(PyExc_TypeError, "setup takes seven addresses and a function");
+    if (n != 9) {
+        PyErr_SetString(PyExc_TypeError, "setup takes seven addresses and two functions");
         return nullptr;
     }
     void* p[7];
@@ -161,6 +172,8 @@ PyObject* setup(PyObject*, PyObject* const* a, Py_ssize_t n) {
     p_mx_weight_grad = reinterpret_cast<decltype(p_mx_weight_grad)>(p[6]);
     Py_INCREF(a[7]);
     Py_XSETREF(raw_stream, a[7]);
+    Py_INCREF(a[8]);
+    Py_XSETREF(current_device, a[8]);
     Py_RETURN_NONE;
 }
 
@@ -219,9 +232,9 @@ PyObject* layer_norm_grad(PyObject*, PyObject* const* av, Py_ssize_t n) {
         if (!a.ok || !code_of(wtype)) Py_RETURN_NONE;
         const int64_t need = dgamma || dbeta ? p_layer_norm_grad_workspace(a.rows, a.width) : 0;
         if (need < 0) Py_RETURN_NONE;
-        const at::Tensor ws = workspace(need, *dy);
         void* s = a.stream();
         if (!a.ok) Py_RETURN_NONE;
+        const at::Tensor ws = workspace(need, *dy);
         return run([&] {
             return p_layer_norm_grad(a.rows, a.width, code_of(type), code_of(wtype), dy->data_ptr(), lddy, x, ldx, gamma,
                                      mean, rstd, dx, lddx, dgamma, dbeta, need ? ws.data_ptr() : nullptr, need, s);
@@ -281,9 +294,9 @@ PyObject* mx_weight_grad(PyObject*, PyObject* const* av, Py_ssize_t n) {
         if (!a.ok) Py_RETURN_NONE;
         const int64_t need = p_mx_weight_grad_workspace(a.rows, out, width);
         if (need < 0) Py_RETURN_NONE;
-        const at::Tensor ws = workspace(need, *dy);
         void* s = a.stream();
         if (!a.ok) Py_RETURN_NONE;
+        const at::Tensor ws = workspace(need, *dy);
         return run([&] {
             return p_mx_weight_grad(a.rows, out, width, code_of(dy->scalar_type()), code_of(dw->scalar_type()), dy->data_ptr(), lddy,
                                     codes, scales, dw->data_ptr(), need ? ws.data_ptr() : nullptr, need, s);
