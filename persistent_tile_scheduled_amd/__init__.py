@@ -165,9 +165,22 @@ def _check(rc: int) -> int:
     return rc
 
 
+_devices = 0   # GPUs that torch sees, asked once
+
+
+def _count_devices() -> int:
+    global _devices
+    import torch
+    _devices = torch.cuda.device_count()
+    return _devices
+
+
 def _enqueue(call, stream, first, *others) -> None:
     """call(handle of `stream`, or of torch's current one) with the tensors' device
     current: the library launches on the current device."""
+    if stream is not None and (_devices or _count_devices()) == 1:
+        _check(call(stream.cuda_stream))
+        return
     import torch
     dev = first.get_device()
     for t in others:
@@ -379,20 +392,22 @@ def _first_call():
     _BOOL = torch.bool
     _FLOATS.update({torch.float16: FP16, torch.bfloat16: BF16, torch.float32: FP32})
     # the same handle as torch.cuda.current_stream(device).cuda_stream without
-    # the Stream object around it (0.1 us instead of 1.8), and the current device
-    # without the question whether torch has begun to use GPUs
+    # the Stream object around it (0.1 us instead of 1.8)
     raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
         (lambda index: torch.cuda.current_stream(index).cuda_stream)
-    device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
     try:
         from . import _tsgemm_torch
     except ImportError as e:
         raise RuntimeError("the binding's extension module is missing: build it with __graft_entry__.build() "
                            "(persistent_tile_scheduled_amd._build.build_torch_module())") from e
     lib = load()
-    _tsgemm_torch.setup(*(ctypes.cast(getattr(lib, "tsgemm_" + name), ctypes.c_void_p).value for name in (
-        "layer_norm", "layer_norm_grad_workspace", "layer_norm_grad", "mx_quantize", "mx_dequantize",
-        "mx_weight_grad_workspace", "mx_weight_grad")), raw_stream, device)
+    addresses = [ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in (
+        "tsgemm_layer_norm", "tsgemm_layer_norm_grad_workspace", "tsgemm_layer_norm_grad", "tsgemm_mx_quantize",
+        "tsgemm_mx_dequantize", "tsgemm_mx_weight_grad_workspace", "tsgemm_mx_weight_grad")]
+    # hipGetDevice by way of the library: that of the runtime it launches with
+    several = (_devices or _count_devices()) != 1
+    addresses.append(ctypes.cast(lib.hipGetDevice, ctypes.c_void_p).value if several else 0)
+    _tsgemm_torch.setup(*addresses, raw_stream)
     _short = _tsgemm_torch
 
 

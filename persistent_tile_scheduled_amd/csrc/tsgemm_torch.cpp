@@ -27,8 +27,8 @@ decltype(&tsgemm_mx_quantize) p_mx_quantize;
 decltype(&tsgemm_mx_dequantize) p_mx_dequantize;
 decltype(&tsgemm_mx_weight_grad_workspace) p_mx_weight_grad_workspace;
 decltype(&tsgemm_mx_weight_grad) p_mx_weight_grad;
-PyObject* raw_stream;      // device index -> handle of torch's current stream
-PyObject* current_device;  // -> device index, on which the C entries launch
+PyObject* raw_stream;             // device index -> handle of torch's current stream
+int (*p_current_device)(int* dev);  // hipGetDevice of the runtime that the library launches with; NULL: one device only
 
 int code_of(at::ScalarType t) {
     return t == at::kHalf ? TSGEMM_FP16 : t == at::kBFloat16 ? TSGEMM_BF16 : t == at::kFloat ? TSGEMM_FP32 : 0;
@@ -109,11 +109,8 @@ struct Args {
     }
     // the stream to launch on, of the tensors' device, which has to be the current one
     void* stream() {
-        PyObject* now = PyObject_CallNoArgs(current_device);
-        const long here = now ? PyLong_AsLong(now) : -1;
-        Py_XDECREF(now);
-        if (here != dev) {
-            PyErr_Clear();
+        int here = -1;
+        if (p_current_device && (p_current_device(&here) != 0 || here != dev)) {
             ok = false;
             return nullptr;
         }
@@ -157,11 +154,11 @@ PyObject* guarded(F&& f) {
 
 PyObject* setup(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (n != 9) {
-        PyErr_SetString(PyExc_TypeError, "setup takes seven addresses and two functions");
+        PyErr_SetString(PyExc_TypeError, "setup takes eight addresses and a function");
         return nullptr;
     }
-    void* p[7];
-    for (int i = 0; i < 7; ++i) p[i] = PyLong_AsVoidPtr(a[i]);
+    void* p[8];
+    for (int i = 0; i < 8; ++i) p[i] = PyLong_AsVoidPtr(a[i]);
     if (PyErr_Occurred()) return nullptr;
     p_layer_norm = reinterpret_cast<decltype(p_layer_norm)>(p[0]);
     p_layer_norm_grad_workspace = reinterpret_cast<decltype(p_layer_norm_grad_workspace)>(p[1]);
@@ -170,10 +167,9 @@ PyObject* setup(PyObject*, PyObject* const* a, Py_ssize_t n) {
     p_mx_dequantize = reinterpret_cast<decltype(p_mx_dequantize)>(p[4]);
     p_mx_weight_grad_workspace = reinterpret_cast<decltype(p_mx_weight_grad_workspace)>(p[5]);
     p_mx_weight_grad = reinterpret_cast<decltype(p_mx_weight_grad)>(p[6]);
-    Py_INCREF(a[7]);
-    Py_XSETREF(raw_stream, a[7]);
+    p_current_device = reinterpret_cast<decltype(p_current_device)>(p[7]);
     Py_INCREF(a[8]);
-    Py_XSETREF(current_device, a[8]);
+    Py_XSETREF(raw_stream, a[8]);
     Py_RETURN_NONE;
 }
 

@@ -21,9 +21,9 @@ import pytest
 c = ctypes
 torch.cuda._lazy_init = lambda: None
 current, calls = [0], []
-torch._C._cuda_getDevice = lambda: current[0]
 torch._C._cuda_getCurrentRawStream = lambda i: 0x1000 * (i + 1)
 torch.cuda.current_device = lambda: current[0]
+torch.cuda.device_count = lambda: 2
 
 
 class device:
@@ -96,7 +96,13 @@ class Library:
                 fake = c.CFUNCTYPE(c.c_int, *f.argtypes)(record)
             setattr(self, name, fake)
 
+def get_device(out):
+    out[0] = current[0]
+    return 0
+
+
 tsg._lib = Library()
+tsg._lib.hipGetDevice = c.CFUNCTYPE(c.c_int, c.POINTER(c.c_int))(get_device)
 
 
 def made(name):
