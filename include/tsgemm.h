@@ -263,8 +263,10 @@ int tsgemm_run_mx_noalloc(const tsgemm_plan* plan, const void* A, const void* SF
  * of their type unless said otherwise.  MX activations are laid out as A and
  * SFA of tsgemm_run_mx: codes uint8[rows][width] (16-byte aligned), scales
  * uint8[rows][width/32] (4-byte aligned), width % 32 == 0.  All pointers are
- * DEVICE pointers owned by the caller, outputs must not overlap inputs, and
- * every call only enqueues work on `stream`.  Sums and statistics are fp32
+ * DEVICE pointers owned by the caller, and every call only enqueues work on
+ * `stream`.  Outputs (a workspace among them) must not overlap inputs or each
+ * other: such a call is refused (TSGEMM_EINVAL).  Matrices that lie between each
+ * other's rows do not overlap.  Sums and statistics are fp32
  * (layer norm's join in fp64); a result is rounded once, to nearest, ties to
  * even.
  *

@@ -377,6 +377,8 @@ class Plan:
 
 
 # ---- what a normalised linear layer needs around the MXFP8 product -----------
+# None of these calls works in place: an output that overlaps an input or another
+# output raises TsgemmError.
 # At the smallest shapes a call costs what the host spends on it.  On torch's
 # current device and stream, with torch's workspaces, the extension module
 # _tsgemm_torch checks the tensors and makes the call; the Python below makes every
@@ -501,7 +503,7 @@ def layer_norm(x, gamma, beta, eps, y=None, mean=None, rstd=None, codes=None, sc
     x[rows, width], written to `y` (x's dtype), or as MX to `codes` and `scales`
     (the A and SFA of run_mx; any 1-byte dtype), or both.  gamma and beta (None:
     ones, zeros) are of x's dtype or float32; mean and rstd, float32[rows], are
-    given together or not at all."""
+    given together or not at all.  No output may overlap an input."""
     if stream is None:
         if _short is None:
             _first_call()
@@ -532,7 +534,8 @@ def layer_norm_grad(dy, x, gamma, mean, rstd, dx, dgamma=None, dbeta=None, works
     (None: not wanted) from dy, x and what layer_norm left in mean and rstd.  dy
     and dx are of x's dtype; gamma (None: ones), dgamma and dbeta share one, x's
     or float32.  `workspace`: a tensor to keep the workgroups' sums in
-    (layer_norm_grad_workspace bytes); by default torch's allocator gives one."""
+    (layer_norm_grad_workspace bytes); by default torch's allocator gives one.  No
+    output may overlap an input (dx is not dy)."""
     if stream is None and workspace is None:
         if _short is None:
             _first_call()

@@ -3,10 +3,12 @@
 #include <hip/hip_runtime.h>
 
 #include <cmath>
+#include <initializer_list>
 
 #include "tsgemm.h"
 #include "tsgemm_host.h"
 #include "tsgemm_ops_launch.h"
+#include "tsgemm_overlap.h"
 #include "tsgemm_rows_kernel.h"
 #include "tsgemm_wgrad_kernel.h"
 
@@ -45,6 +47,30 @@ int check_mx(int64_t width, const void* codes, const void* scales) {
     if (width % 32 != 0) return fail(TSGEMM_EINVAL, "MX blocks need a width divisible by 32, got %lld", (long long)width);
     if (!codes || !scales) return fail(TSGEMM_EINVAL, "codes or scales is NULL");
     if (off(codes, 16) || off(scales, 4)) return fail(TSGEMM_EINVAL, "codes must be 16-byte and scales 4-byte aligned");
+    return TSGEMM_OK;
+}
+struct Named {
+    const char* name;
+    tsg::Region r;
+    tsg::Extent e;
+};
+Named matrix(const char* name, const void* p, int64_t rows, int64_t width, int64_t ld, int bytes) {
+    const tsg::Region r = {p, rows, width * bytes, ld * bytes};
+    return {name, r, tsg::extent(r)};
+}
+Named stretch(const char* name, const void* p, int64_t bytes) { return matrix(name, p, 1, bytes, bytes, 1); }
+// No output over an input or another output: workgroups read rows, some of them
+// twice, while others already write.
+int check_overlaps(std::initializer_list<Named> outputs, std::initializer_list<Named> inputs) {
+    const auto clash = [](const Named& o, const Named& other) {  // nearly always the extents say no
+        return o.e.from < other.e.to && other.e.from < o.e.to && tsg::overlap(o.r, other.r);
+    };
+    for (const Named& o : outputs) {
+        for (const Named& i : inputs)
+            if (clash(o, i)) return fail(TSGEMM_EINVAL, "%s overlaps %s", o.name, i.name);
+        for (const Named* other = outputs.begin(); other != &o; ++other)
+            if (clash(o, *other)) return fail(TSGEMM_EINVAL, "%s overlaps %s", o.name, other->name);
+    }
     return TSGEMM_OK;
 }
 int launched(const char* what) {
@@ -89,6 +115,11 @@ int tsgemm_layer_norm(int64_t rows, int64_t width, int dtype, int weight_dtype, 
     if (!mean != !rstd) return fail(TSGEMM_EINVAL, "mean and rstd are given together or not at all");
     if (off(mean, 4) || off(rstd, 4) || off(gamma, (unsigned)bytes_of(weight_dtype)) || off(beta, (unsigned)bytes_of(weight_dtype)))
         return fail(TSGEMM_EINVAL, "gamma, beta, mean and rstd must be aligned to their types");
+    const int e = bytes_of(dtype), we = bytes_of(weight_dtype);
+    rc = check_overlaps({matrix("y", y, rows, width, ldy, e), stretch("mean", mean, 4 * rows), stretch("rstd", rstd, 4 * rows),
+                         stretch("codes", codes, rows * width), stretch("scales", scales, rows * (width / 32))},
+                        {matrix("x", x, rows, width, ldx, e), stretch("gamma", gamma, we * width), stretch("beta", beta, we * width)});
+    if (rc != TSGEMM_OK) return rc;
     tsg::LnArgs a = {};
     a.x = x; a.gamma = gamma; a.beta = beta; a.y = y; a.mean = mean; a.rstd = rstd;
     a.codes = static_cast<uint8_t*>(codes); a.scales = static_cast<uint8_t*>(scales);
@@ -129,6 +160,12 @@ int tsgemm_layer_norm_grad(int64_t rows, int64_t width, int dtype, int weight_dt
         if (sums && (!workspace || off(workspace, 16) || workspace_bytes < need))
             return fail(TSGEMM_EINVAL, "dgamma and dbeta need a 16-byte aligned workspace of %lld bytes", (long long)need);
     }
+    const int e = bytes_of(dtype), we = bytes_of(weight_dtype);
+    rc = check_overlaps({matrix("dx", dx, rows, width, lddx, e), stretch("dgamma", dgamma, we * width),
+                         stretch("dbeta", dbeta, we * width), stretch("workspace", sums ? workspace : nullptr, need)},
+                        {matrix("dy", dy, rows, width, lddy, e), matrix("x", x, rows, width, ldx, e),
+                         stretch("gamma", gamma, we * width), stretch("mean", mean, 4 * rows), stretch("rstd", rstd, 4 * rows)});
+    if (rc != TSGEMM_OK) return rc;
     const hipStream_t s = static_cast<hipStream_t>(stream);
     const bool small = rows > 0 && tsg::layer_norm_grad_small(rows, (uint32_t)width);
     float* part = sums && !small ? static_cast<float*>(workspace) : nullptr;
@@ -157,6 +194,9 @@ int tsgemm_mx_quantize(int64_t rows, int64_t width, int dtype, const void* x, in
     if (rows == 0 || width == 0) return TSGEMM_OK;
     rc = check_matrix("x", x, ldx, width, dtype);
     if (rc == TSGEMM_OK) rc = check_mx(width, codes, scales);
+    if (rc == TSGEMM_OK)
+        rc = check_overlaps({stretch("codes", codes, rows * width), stretch("scales", scales, rows * (width / 32))},
+                            {matrix("x", x, rows, width, ldx, bytes_of(dtype))});
     if (rc != TSGEMM_OK) return rc;
     (void)hipGetLastError();
     tsg::launch_mx_quantize(dtype, x, ldx, rows, (uint32_t)width, static_cast<uint8_t*>(codes), static_cast<uint8_t*>(scales),
@@ -173,6 +213,9 @@ int tsgemm_mx_dequantize(int64_t rows, int64_t width, int dtype, const void* cod
     if (rows == 0 || width == 0) return TSGEMM_OK;
     rc = check_matrix("out", out, ldo, width, dtype);
     if (rc == TSGEMM_OK) rc = check_mx(width, codes, scales);
+    if (rc == TSGEMM_OK)
+        rc = check_overlaps({matrix("out", out, rows, width, ldo, bytes_of(dtype))},
+                            {stretch("codes", codes, rows * width), stretch("scales", scales, rows * (width / 32))});
     if (rc != TSGEMM_OK) return rc;
     (void)hipGetLastError();
     tsg::launch_mx_dequantize(dtype, static_cast<const uint8_t*>(codes), static_cast<const uint8_t*>(scales), rows, (uint32_t)width,
@@ -205,6 +248,10 @@ int tsgemm_mx_weight_grad(int64_t rows, int64_t out, int64_t width, int dtype, i
         if (lddy >= (int64_t(1) << 24)) return fail(TSGEMM_EUNSUPPORTED, "dy's row stride must be below 2^24 (32-bit offsets in a slab of 64 rows)");
         if (need > 0 && (!workspace || off(workspace, 16) || workspace_bytes < need))
             return fail(TSGEMM_EINVAL, "this shape needs a 16-byte aligned workspace of %lld bytes", (long long)need);
+        rc = check_overlaps({stretch("dw", dw, out * width * bytes_of(grad_dtype)), stretch("workspace", workspace, need)},
+                            {matrix("dy", dy, rows, out, lddy, 2), stretch("codes", codes, rows * width),
+                             stretch("scales", scales, rows * (width / 32))});
+        if (rc != TSGEMM_OK) return rc;
     }
     tsg::WgradArgs a = {};
     a.dy = static_cast<const uint16_t*>(dy); a.codes = static_cast<const uint8_t*>(codes);
