@@ -317,11 +317,14 @@ int tsgemm_mx_dequantize(int64_t rows, int64_t width, int dtype, const void* cod
  *   dy[rows][out] is TSGEMM_FP16 or TSGEMM_BF16 (`dtype`), its rows 16-byte
  *   aligned (out % 8 == 0, lddy % 8 == 0); dw[out][width] is contiguous, 16-byte
  *   aligned, of dtype or TSGEMM_FP32 (`grad_dtype`).  The terms keep all bits
- *   of both factors; the sum is fp32.  Shapes with few tiles of dw split the
- *   rows over workgroups and need `workspace` (16-byte aligned,
- *   tsgemm_mx_weight_grad_workspace bytes, possibly 0); the result of a shape
- *   is the same bits every time.  rows == 0 makes dw zero, out * width == 0
- *   launches nothing. */
+ *   of dy and of code * scale, where that is a bf16 value: with scale codes
+ *   0 ... 2 it is rounded to bf16's last place, 2^-133, and from 2^128 on it is
+ *   an infinity, as in fp32.  The sum is fp32; with fp16 dy it is held times 2^6,
+ *   so that from 2^122 on (only scales past 2^32 come there) it is an infinity.
+ *   Shapes with few tiles of dw split the rows over workgroups and need
+ *   `workspace` (16-byte aligned, tsgemm_mx_weight_grad_workspace bytes, possibly
+ *   0); the result of a shape is the same bits every time.  rows == 0 makes dw
+ *   zero, out * width == 0 launches nothing. */
 int64_t tsgemm_mx_weight_grad_workspace(int64_t rows, int64_t out, int64_t width);
 int tsgemm_mx_weight_grad(int64_t rows, int64_t out, int64_t width, int dtype, int grad_dtype, const void* dy,
                           int64_t lddy, const void* codes, const void* scales, void* dw, void* workspace,

@@ -6,15 +6,18 @@
 // Formats specification v1.0).  The sum runs over the rows, across which the
 // scales change, so the block-scaled matrix instruction (one scale per 32 terms
 // of the sum) cannot take them: the codes are decoded on their way into LDS.
-//   * bf16 dy: to bf16, which holds every element times scale of the fp32 range
-//     exactly.
+//   * bf16 dy: to bf16, which holds every element times scale exactly from scales
+//     of 2^-124 (code 3; its last place is 2^-133, that of the elements 2^-9) up to
+//     2^128, where fp32 ends too.
 //   * fp16 dy: to fp16, times 2^kShift, which dw is divided by in the end.  That
 //     is exact for scales of 2^kScaleLow ... 2^kScaleHigh: the least element
 //     2^-9 becomes at least fp16's least 2^-24, the largest 448 at most 57344.
 //     Blocks of activations whose largest magnitude is between 2^-13 and 2^10
 //     have such scales.  A 64-row slab with a block outside (other than one of
 //     zeros) is multiplied in bf16 instead, with dy split into two bf16 values
-//     whose sum it is, at half the rate: no term loses a bit either way.
+//     whose sum it is, at half the rate: no term loses a bit either way, but for
+//     the ends that bf16 has above.  The factor 2^kShift stays in the accumulators,
+//     so a sum of far terms overflows from 2^122 on.
 //
 // Both operands lie with the sum's index slowest, [row][column], and both come
 // out of LDS through the transpose read ds_read_b64_tr_b16.  One workgroup of

@@ -193,3 +193,29 @@ def test_fp16_every_code_about_the_borders(fields):
         dw = torch.empty((256, 256), device=DEV)
         tsg.mx_weight_grad(d, codes, scales, dw)
         assert torch.equal(dw.double(), own.double()[:, None] * _values(codes, scales)), part
+
+
+@pytest.mark.parametrize("dtype", [FP16, BF16], ids=str)
+def test_the_ends_of_the_range(dtype):
+    """Scale codes 0 ... 2, where code * scale is rounded to bf16's subnormals, 3,
+    from which it is exact, and the top, where it ends with fp32; fp16's sums end
+    at 2^122.  One term an element, rows of one scale each alone."""
+    codes = torch.arange(256, dtype=torch.uint8, device=DEV).repeat(64, 1)
+    codes[:, 0x7F] = 0
+    codes[:, 0xFF] = 0
+    element = _elements()[codes[0].long()]
+    for field in (0, 1, 2, 3, 4, 30, 230, 245, 246, 250):
+        value = element * 2.0 ** (field - 127)
+        held = value.float().bfloat16().double()
+        assert torch.equal(held, value) or field < 3 or field > 246
+        for power in (-10, 0, 10):
+            d = torch.zeros((64, 8), dtype=dtype, device=DEV)
+            d[5, 3] = 2.0 ** power
+            dw = torch.empty((8, 256), device=DEV)
+            tsg.mx_weight_grad(d, codes, torch.full((64, 8), field, dtype=torch.uint8, device=DEV), dw)
+            want = held * 2.0 ** power
+            end = 2.0 ** (122 if dtype == FP16 else 128)
+            want = torch.where(want.abs() >= end, torch.sign(want) * float("inf"), want)
+            value_ends = held.abs() >= 2.0 ** 128          # times the other rows' zeros: no number
+            assert torch.equal(dw[3].double()[~value_ends], want[~value_ends]), (field, power)
+            assert torch.isnan(dw[3][value_ends]).all()
