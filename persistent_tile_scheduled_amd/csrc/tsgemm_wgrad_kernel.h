@@ -87,6 +87,27 @@ __device__ __forceinline__ void mfma_bf16_settled(f32x4& acc, i16x8 a, i16x8 b) 
     asm volatile("s_nop 1\n\tv_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(acc) : "v"(a), "v"(b));
 }
 
+// Race-detection build (TSG_STRESS): a pause of 0 to ~2048 cycles, as stress_pause,
+// whose length comes from a linear congruential sequence that each wave starts
+// elsewhere.  All of it is one asm block: branches or arithmetic that the compiler
+// sees at every pause take the registers that the accumulators need, which it then
+// copies right beside MFMAs that it cannot see to wait for.  The count only falls,
+// so the loop ends.
+__device__ __forceinline__ uint32_t pause_seed(uint32_t wave) { return (blockIdx.x * 4u + wave + 1u) * 0x9E3779B1u; }
+__device__ __forceinline__ void wgrad_pause(uint32_t& state) {
+#if TSG_STRESS
+    uint32_t count;  // 0, 0, 0, 1, 2, 4, 8 or 16 times 128 cycles
+    asm volatile(
+        "s_mul_i32 %0, %0, 0x19660d\n\ts_add_u32 %0, %0, 0x3c6ef35f\n\t"
+        "s_lshr_b32 %1, %0, 29\n\ts_lshl_b32 %1, 1, %1\n\ts_lshr_b32 %1, %1, 3\n"
+        ".Lpause%=:\n\ts_cmp_eq_u32 %1, 0\n\ts_cbranch_scc1 .Lon%=\n\ts_sleep 2\n\ts_sub_u32 %1, %1, 1\n\t"
+        "s_branch .Lpause%=\n.Lon%=:"
+        : "+s"(state), "=&s"(count)::"scc", "memory");
+#else
+    (void)state;
+#endif
+}
+
 // 8 fp16 values times 2^kShift = hi + lo in bf16, exactly (11 significant bits in 8 + 3).
 __device__ __forceinline__ void split_f16(i16x8 v, i16x8& hi, i16x8& lo) {
     const f16x8 x = __builtin_bit_cast(f16x8, v);
@@ -112,14 +133,8 @@ __global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void wgrad_kernel(WgradArgs
     const uint32_t lds_base = (uint32_t)reinterpret_cast<uintptr_t>((lds_u8*)smem);
     const uint32_t lane = threadIdx.x & 63u;
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    // Race-detection build only (TSG_STRESS), and not for fp16: its two pipelines
-    // with a branch at every pause leave the compiler too few accumulators, which
-    // it then copies right beside the MFMAs in asm that it cannot see to wait for.
-    // What bf16's pipeline waits for, fp16's does too.
-    uint32_t stress_ctr = 0;
-    auto pause = [&](auto site_c) __attribute__((always_inline)) {
-        if constexpr (DT == DT_BF16) stress_pause<decltype(site_c)::value>(wave, stress_ctr);
-    };
+    uint32_t pauses = pause_seed(wave);  // race-detection build only
+    auto pause = [&]() __attribute__((always_inline)) { wgrad_pause(pauses); };
     const uint32_t wr = wave >> 1, wc = wave & 1u;
     const uint32_t out = args.out, width = args.width, w32 = width / 32u;
 
@@ -180,7 +195,7 @@ __global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void wgrad_kernel(WgradArgs
     }
     auto dma = [&](auto q_c, auto s_c) __attribute__((always_inline)) {
         constexpr int q = decltype(q_c)::value, S = decltype(s_c)::value;
-        pause(std::integral_constant<int, 2>{});
+        pause();
         dma16_at<(uint32_t)(S * T::A_STAGE + q * 1024)>(lds_base + wave * NA * 1024u, a_voff[q], rs_a);
     };
 
@@ -364,11 +379,14 @@ __global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void wgrad_kernel(WgradArgs
     auto period = [&](auto mode_c, auto s_c, uint32_t next, uint32_t& end) __attribute__((always_inline)) {
         constexpr int MODE = decltype(mode_c)::value, S = decltype(s_c)::value;
         using OTHER = std::integral_constant<int, 1 - S>;
-        pause(std::integral_constant<int, 0>{});
+        pause();
         wait_vm<0>();    // the next slab's dy and the codes after it have landed
-        if constexpr (MODE == WG_FP16) put_flag(s_c);
+        if constexpr (MODE == WG_FP16) {
+            put_flag(s_c);
+            pause();
+        }
         lds_barrier();   // ... for every wave; stage S is read out, its successor written
-        pause(std::integral_constant<int, 1>{});
+        pause();
         next_a();
         next_c();
         kstep(mode_c, I1{}, [&](auto g_c) __attribute__((always_inline)) {
@@ -380,7 +398,10 @@ __global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void wgrad_kernel(WgradArgs
             }
         });
         bool far = false;
-        if constexpr (MODE == WG_FP16) far = get_flag(s_c);
+        if constexpr (MODE == WG_FP16) {
+            pause();
+            far = get_flag(s_c);
+        }
         kstep(mode_c, I0{}, [&](auto g_c) __attribute__((always_inline)) {
             constexpr int g = decltype(g_c)::value;
             if constexpr (g >= START)
@@ -413,12 +434,16 @@ __global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void wgrad_kernel(WgradArgs
         static_for<0, 4 * NP>([&](auto i_c) __attribute__((always_inline)) { convert(mode_c, I1{}, i_c); });
         next_c();
         static_for<0, 3 * NP>([&](auto i_c) __attribute__((always_inline)) { load_codes(I0{}, i_c); });
+        pause();
         wait_vm<0>();
         lds_barrier();
+        pause();
         uint32_t end = to;
         if constexpr (MODE == WG_FP16) {
             const bool far0 = get_flag(I0{}), far1 = get_flag(I1{});
+            pause();
             lds_barrier();  // the flags are read before the first period's
+            pause();
             if (far0) return from;
             if (far1 && from + 1u < end) end = from + 1u;
         }
@@ -438,8 +463,10 @@ __global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void wgrad_kernel(WgradArgs
         }
         kstep(mode_c, I1{}, [](auto) __attribute__((always_inline)) {});
         gap_nops();      // the last MFMAs have written their accumulators
+        pause();
         wait_vm<0>();    // no DMA may still target LDS when the next pipeline starts or the workgroup retires
         lds_barrier();
+        pause();
         return end;
     };
 
