@@ -111,6 +111,15 @@ def build_library(out: str = OUT, verbose: bool = False, extra_flags=()) -> str:
     return out
 
 
+def main(argv) -> None:
+    """What the package loads, or with --stress the race-detection library."""
+    if "--stress" in argv:
+        print(build_stress_library())
+    else:
+        print(build_library())
+        print(build_torch_module())
+
+
 if __name__ == "__main__":
     import sys
-    print(build_stress_library() if "--stress" in sys.argv[1:] else build_library())
+    main(sys.argv[1:])
