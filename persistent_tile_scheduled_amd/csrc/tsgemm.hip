@@ -50,9 +50,6 @@ namespace {
 thread_local char g_err[512] = "";
 thread_local int g_code = 0;
 
-std::atomic<int> g_cu_count[64];
-std::atomic<int> g_xcd_count[64];
-
 }  // namespace
 
 namespace tsg {
@@ -72,42 +69,10 @@ int fail(int code, const char* fmt, ...) {
     return code;
 }
 
-// Persistent grid default: one workgroup per compute unit of the device; the
-// XCD count (accelerator complex dies, each with its own L2) drives the
-// worker renumbering.  Both are queried once per device and cached.
-int device_cus(int* cus, int* xcds) {
-    int dev = 0;
-    hipError_t e = hipGetDevice(&dev);
-    if (e != hipSuccess) return fail(TSGEMM_EHIP, "hipGetDevice: %s", hipGetErrorString(e));
-    const bool cached = dev >= 0 && dev < 64;
-    int n = cached ? g_cu_count[dev].load() : 0;
-    int x = cached ? g_xcd_count[dev].load() : 0;
-    if (n <= 0 || x <= 0) {
-        e = hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev);
-        if (e != hipSuccess || n <= 0)
-            return fail(TSGEMM_EHIP, "cannot query the compute-unit count: %s", hipGetErrorString(e));
-        // Workgroup b of a launch goes to XCD b % (XCD count).  A runtime that
-        // cannot report the count gets 1: the renumbering is then the
-        // identity, which changes speed only, never C or the schedule.
-        if (hipDeviceGetAttribute(&x, hipDeviceAttributeNumberOfXccs, dev) != hipSuccess || x <= 0) {
-            (void)hipGetLastError();
-            x = 1;
-        }
-        if (cached) {
-            g_cu_count[dev].store(n);
-            g_xcd_count[dev].store(x);
-        }
-    }
-    *cus = n;
-    *xcds = x;
-    return TSGEMM_OK;
-}
-
 }  // namespace tsg
 
 namespace {
 
-using tsg::device_cus;
 using tsg::fail;
 using tsg::reset_error;
 using tsg::KernelEntry;
@@ -164,6 +129,40 @@ int ring_slots(int bm, int bn, int bk, int stages, int epi = 0) {
 bool tile_supported(int bm, int bn, int bk) {
     return (bm == 128 && bn == 128 && (bk == 32 || bk == 64)) ||
            (bm == 256 && bn == 256 && (bk == 32 || bk == 64));
+}
+
+// Persistent grid default: one workgroup per compute unit of the device; the
+// XCD count (accelerator complex dies, each with its own L2) drives the
+// worker renumbering.  Both are queried once per device and cached.
+std::atomic<int> g_cu_count[64];
+std::atomic<int> g_xcd_count[64];
+
+int device_cus(int* cus, int* xcds) {
+    int dev = 0;
+    hipError_t e = hipGetDevice(&dev);
+    if (e != hipSuccess) return fail(TSGEMM_EHIP, "hipGetDevice: %s", hipGetErrorString(e));
+    const bool cached = dev >= 0 && dev < 64;
+    int n = cached ? g_cu_count[dev].load() : 0;
+    int x = cached ? g_xcd_count[dev].load() : 0;
+    if (n <= 0 || x <= 0) {
+        e = hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev);
+        if (e != hipSuccess || n <= 0)
+            return fail(TSGEMM_EHIP, "cannot query the compute-unit count: %s", hipGetErrorString(e));
+        // Workgroup b of a launch goes to XCD b % (XCD count).  A runtime that
+        // cannot report the count gets 1: the renumbering is then the
+        // identity, which changes speed only, never C or the schedule.
+        if (hipDeviceGetAttribute(&x, hipDeviceAttributeNumberOfXccs, dev) != hipSuccess || x <= 0) {
+            (void)hipGetLastError();
+            x = 1;
+        }
+        if (cached) {
+            g_cu_count[dev].store(n);
+            g_xcd_count[dev].store(x);
+        }
+    }
+    *cus = n;
+    *xcds = x;
+    return TSGEMM_OK;
 }
 
 }  // namespace

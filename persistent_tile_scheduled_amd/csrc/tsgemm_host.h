@@ -11,7 +11,4 @@ void reset_error();
 // tsgemm_last_error_code of this thread, and returns the code.
 int fail(int code, const char* fmt, ...);
 
-// Compute units and XCDs of the current device; 0 or a TSGEMM_E* code.
-int device_cus(int* cus, int* xcds);
-
 }  // namespace tsg
