@@ -31,11 +31,13 @@
 // With few tiles the rows are split over workgroups, whose fp32 tiles a second
 // launch adds up in order.
 //
-// Measured: 8192^3 bf16 741-765 us, 1440-1484 TFLOP/s (the library's bf16 product
-// of that size 1291 on the same card), bound by the board's power: 1380 W of
-// 1400, clocks down to 2.1 GHz; fp16 823 us, 1336 (library 1223).  32768 x 2048 x
-// 2048 in 4 splits 214 us, of which the products' way through memory takes 25.
-// 512^3 fp16 9.3 us: 16 workgroups, 8 slabs each, every one a round trip.
+// Measured, over several boxes: 8192^3 bf16 741-795 us, 1383-1484 TFLOP/s (the
+// library's bf16 product of that size 1238-1413), bound by the board's power: 1380 W
+// of 1400, clocks down to 2.1 GHz; fp16 811-859 us (library 1223-1339 TFLOP/s, 821-899
+// us).  32768 x 2048 x 2048 in 4 splits 212 us, of which the products' way through
+// memory takes 25.  512^3 fp16 9.1 us: 16 workgroups, 8 slabs each, every one a round
+// trip.  4096 x 2048 x 2048 bf16 56.5 us with its operands in HBM, 46.4 in the cache;
+// there dequantizing and the library's product take 49.2.
 //
 // Built and not kept for the 128 x 128 tile: four stages of dy with three slabs on
 // their way.  One workgroup alone went from 0.53 to 0.43 us a slab, 256 of them

@@ -19,10 +19,10 @@ struct WgradShape {
 // the slabs of one (1.4 of a large tile; of a small one 0.56 alone and 0.95 beside
 // another) and a start of 3, plus a second launch of 3, the splits' fp32 products
 // written and read at 4 TB/s and 0.03 a split for adding them up.  Measured with
-// both sides of each choice: 4096 x 2048 x 2048 bf16 small tiles unsplit 45,
-// large ones in 4 splits 51; 32768 x 2048 x 2048 large in 4 splits 212, small in 2
-// 273; 65536 x 64 x 64 small in 64, 128 and 256 splits 16.3, 13.3 and 13.9;
-// 512^3 small unsplit 8.5, in 2 splits 9.9.
+// both sides of each choice, operands in the cache: 4096 x 2048 x 2048 bf16 small
+// tiles unsplit 45, large ones in 4 splits 51; 32768 x 2048 x 2048 large in 4 splits
+// 212, small in 2 273; 65536 x 64 x 64 small in 64, 128 and 256 splits 16.3, 13.3 and
+// 13.9; 512^3 small unsplit 8.5, in 2 splits 9.9.
 inline WgradShape wgrad_shape(int64_t rows, int64_t out, int64_t width) {
     constexpr int64_t kCus = 256;  // MI355X
     WgradShape best = {};
