@@ -330,6 +330,75 @@ int tsgemm_mx_weight_grad(int64_t rows, int64_t out, int64_t width, int dtype, i
                           int64_t lddy, const void* codes, const void* scales, void* dw, void* workspace,
                           int64_t workspace_bytes, void* stream);
 
+/* ---- what a language model's linear layers need next to the products --------
+ *
+ * The conventions of the calls above (row strides, DEVICE pointers, nothing but
+ * work enqueued on `stream`, no output over an input or another output).  All
+ * matrices are of one 16-bit `dtype`, TSGEMM_FP16 or TSGEMM_BF16.  x, the weights
+ * and their gradients have 16-byte aligned rows: width a positive multiple of 8,
+ * row strides multiples of 8 below 2^23.  The other matrices need only the
+ * alignment of their type, so rows, hidden and vocab may be any number (hidden and
+ * vocab below 2^30, no matrix of 2^40 values).  Products are summed in fp32.  What
+ * a shape gives is the same bits every time.
+ *
+ * tsgemm_gated_linear: both projections of a gated feed-forward layer, its
+ * activation and their product,
+ *     g = x * gate_weight^T    u = x * up_weight^T    y = act(g) * u
+ *   with x[rows][width], gate_weight and up_weight[hidden][width], y[rows][hidden];
+ *   act is TSGEMM_SILU (g / (1 + exp(-g))), TSGEMM_GELU (g times the normal
+ *   distribution function) or TSGEMM_GELU_TANH (its approximation by tanh).  g and
+ *   u are fp32 until y is rounded.  gate and up (each may be NULL: not kept) are g
+ *   and u rounded to dtype, what the gradient reads.  rows * hidden == 0 launches
+ *   nothing. */
+enum { TSGEMM_SILU = 1, TSGEMM_GELU = 2, TSGEMM_GELU_TANH = 3 };
+int tsgemm_gated_linear(int64_t rows, int64_t hidden, int64_t width, int dtype, int act, const void* x, int64_t ldx,
+                        const void* gate_weight, int64_t ldgw, const void* up_weight, int64_t lduw, void* y, int64_t ldy,
+                        void* gate, int64_t ldgate, void* up, int64_t ldup, void* stream);
+
+/* Its gradient, from gate and up as tsgemm_gated_linear kept them:
+ *     dg = dy * up * act'(gate)    du = dy * act(gate)
+ *     dx = dg * gate_weight + du * up_weight
+ *     dgate_weight = dg^T * x      dup_weight = du^T * x
+ *   dg and du are rounded to dtype, as the gradients of a 16-bit tensor are (in
+ *   fp16 a value past 65504 is an infinity), before the products sum them in fp32.
+ *   dx may be NULL, or dgate_weight and dup_weight together (not wanted).
+ *   `workspace` is 16-byte aligned, of at least tsgemm_gated_linear_grad_workspace
+ *   bytes, contents irrelevant.  Without rows the weights' gradients are zero,
+ *   without hidden columns dx is.  hidden is below 2^22. */
+int64_t tsgemm_gated_linear_grad_workspace(int64_t rows, int64_t hidden, int64_t width);
+int tsgemm_gated_linear_grad(int64_t rows, int64_t hidden, int64_t width, int dtype, int act, const void* dy, int64_t lddy,
+                             const void* x, int64_t ldx, const void* gate_weight, int64_t ldgw, const void* up_weight,
+                             int64_t lduw, const void* gate, int64_t ldgate, const void* up, int64_t ldup, void* dx,
+                             int64_t lddx, void* dgate_weight, int64_t lddgw, void* dup_weight, int64_t ldduw, void* workspace,
+                             int64_t workspace_bytes, void* stream);
+
+/* The softmax cross entropy of a linear head, without its logits in memory:
+ *     l = x * weight^T    lse = log(sum_v exp(l[v]))    loss = lse - l[target]
+ *   per row, with x[rows][width], weight[vocab][width], target int64[rows], loss
+ *   and lse fp32[rows].  A row whose target is ignore_index has loss 0; one whose
+ *   target is neither that nor in [0, vocab) has a NaN loss.  An infinite or NaN
+ *   logit makes its row's loss and lse NaN.  vocab >= 1; rows == 0 launches nothing.
+ *   `workspace` as above, tsgemm_linear_cross_entropy_workspace bytes. */
+int64_t tsgemm_linear_cross_entropy_workspace(int64_t rows, int64_t vocab, int64_t width);
+int tsgemm_linear_cross_entropy(int64_t rows, int64_t vocab, int64_t width, int dtype, const void* x, int64_t ldx,
+                                const void* weight, int64_t ldw, const int64_t* target, int64_t ignore_index, float* loss,
+                                float* lse, void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Its gradient, from lse as tsgemm_linear_cross_entropy wrote it and dloss, the
+ * gradient of every row's loss (fp32[rows]):
+ *     dl = dloss * (exp(l - lse) - (v == target))    dx = dl * weight    dweight = dl^T * x
+ *   A row whose target is ignore_index or outside the vocabulary counts for nothing,
+ *   whatever x, lse and dloss hold there: its dl is zero, and dweight has no term of
+ *   it.  The logits are formed again, piece by piece of the vocabulary; of a piece
+ *   dl is held in `workspace`, rounded to dtype (in fp16 times a power of two that
+ *   makes the largest |dloss| about 2^13, which dx and dweight are divided by).  dx
+ *   or dweight may be NULL (not wanted).  rows == 0 makes dweight zero. */
+int64_t tsgemm_linear_cross_entropy_grad_workspace(int64_t rows, int64_t vocab, int64_t width);
+int tsgemm_linear_cross_entropy_grad(int64_t rows, int64_t vocab, int64_t width, int dtype, const float* dloss, const void* x,
+                                     int64_t ldx, const void* weight, int64_t ldw, const int64_t* target,
+                                     int64_t ignore_index, const float* lse, void* dx, int64_t lddx, void* dweight,
+                                     int64_t lddw, void* workspace, int64_t workspace_bytes, void* stream);
+
 /* m_blocks * n_blocks, the tile count the scheduler walks (page "[Feature]
  * Introduce tile scheduler #2441", Files changed: the waves formula
  * ceildiv(m_blocks * n_blocks, sm_num)); < 0 on error. */

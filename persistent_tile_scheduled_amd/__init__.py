@@ -9,7 +9,8 @@ Names follow the C ABI: ``create`` -> :class:`Plan`, ``Plan.run``,
 ``Plan.run_traced``, ``Plan.run_mx``, ``Plan.run_mx_traced``,
 ``Plan.dump_schedule``, ``Plan.schedule_host``, ``Plan.info``, ``last_error``,
 ``layer_norm``, ``layer_norm_grad``, ``mx_quantize``, ``mx_dequantize``,
-``mx_weight_grad``.
+``mx_weight_grad``, ``gated_linear``, ``gated_linear_grad``,
+``linear_cross_entropy``, ``linear_cross_entropy_grad``.
 """
 
 from __future__ import annotations
@@ -40,6 +41,9 @@ EXPORTS = (
     "tsgemm_last_error_code", "tsgemm_launch_info", "tsgemm_run_mx_noalloc", "tsgemm_worker_numbering",
     "tsgemm_layer_norm", "tsgemm_layer_norm_grad_workspace", "tsgemm_layer_norm_grad", "tsgemm_mx_quantize",
     "tsgemm_mx_dequantize", "tsgemm_mx_weight_grad_workspace", "tsgemm_mx_weight_grad",
+    "tsgemm_gated_linear", "tsgemm_gated_linear_grad_workspace", "tsgemm_gated_linear_grad",
+    "tsgemm_linear_cross_entropy_workspace", "tsgemm_linear_cross_entropy",
+    "tsgemm_linear_cross_entropy_grad_workspace", "tsgemm_linear_cross_entropy_grad",
 )
 
 
@@ -150,6 +154,20 @@ def load(path: str | None = None):
     lib.tsgemm_mx_weight_grad_workspace.restype = i64
     lib.tsgemm_mx_weight_grad.argtypes = [i64, i64, i64, i32, i32, vp, i64, vp, vp, vp, vp, i64, vp]
     lib.tsgemm_mx_weight_grad.restype = i32
+    lib.tsgemm_gated_linear.argtypes = [i64, i64, i64, i32, i32] + [vp, i64] * 6 + [vp]
+    lib.tsgemm_gated_linear.restype = i32
+    lib.tsgemm_gated_linear_grad_workspace.argtypes = [i64, i64, i64]
+    lib.tsgemm_gated_linear_grad_workspace.restype = i64
+    lib.tsgemm_gated_linear_grad.argtypes = [i64, i64, i64, i32, i32] + [vp, i64] * 10 + [vp]
+    lib.tsgemm_gated_linear_grad.restype = i32
+    lib.tsgemm_linear_cross_entropy_workspace.argtypes = [i64, i64, i64]
+    lib.tsgemm_linear_cross_entropy_workspace.restype = i64
+    lib.tsgemm_linear_cross_entropy.argtypes = [i64, i64, i64, i32, vp, i64, vp, i64, vp, i64, vp, vp, vp, i64, vp]
+    lib.tsgemm_linear_cross_entropy.restype = i32
+    lib.tsgemm_linear_cross_entropy_grad_workspace.argtypes = [i64, i64, i64]
+    lib.tsgemm_linear_cross_entropy_grad_workspace.restype = i64
+    lib.tsgemm_linear_cross_entropy_grad.argtypes = [i64, i64, i64, i32, vp, vp, i64, vp, i64, vp, i64, vp, vp, i64, vp, i64, vp, i64, vp]
+    lib.tsgemm_linear_cross_entropy_grad.restype = i32
     if path is None:
         _lib = lib
     return lib
@@ -619,6 +637,139 @@ def mx_weight_grad(dy, codes, scales, dw, workspace=None, stream=None) -> None:
 def mx_weight_grad_workspace(rows: int, out: int, width: int) -> int:
     """Bytes of workspace an mx_weight_grad of this shape takes (0: none)."""
     return _check(load().tsgemm_mx_weight_grad_workspace(rows, out, width))
+
+
+# ---- what a language model's linear layers need next to the products ---------
+# As the calls above: rows with contiguous values, no output over an input or
+# another output, workspaces of torch's allocator unless one is given.
+ACTS = {"silu": 1, "gelu": 2, "gelu_tanh": 3}
+
+
+def _act_code(act):
+    code = ACTS.get(act)
+    if code is None:
+        raise ValueError(f"act must be one of {', '.join(ACTS)}, got {act!r}")
+    return code
+
+
+def _x_16bit(x):
+    """dtype and its code, rows, width, device index and row stride of the activation x."""
+    dt = _dtype_code("x", x.dtype)
+    if dt == FP32:
+        raise ValueError(f"x must be float16 or bfloat16, got {x.dtype}")
+    return (x.dtype, dt) + _rows_width("x", x)
+
+
+def _maybe_matrix(name, t, shape, dtype, dev):
+    return (None, 0) if t is None else _matrix(name, t, shape, dtype, dev)
+
+
+def _weight(name, t, width, dtype, dev):
+    """Rows, pointer and row stride of a weight."""
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have two dimensions")
+    return (t.shape[0],) + _matrix(name, t, (t.shape[0], width), dtype, dev)
+
+
+def gated_linear(x, gate_weight, up_weight, y, act="silu", gate=None, up=None, stream=None) -> None:
+    """tsgemm_gated_linear: y[rows, hidden] = act(x @ gate_weight^T) * (x @ up_weight^T)
+    with x[rows, width], gate_weight and up_weight[hidden, width], all float16 or all
+    bfloat16.  act is "silu", "gelu" or "gelu_tanh".  gate and up (None: not kept)
+    receive the two projections, which the gradient needs.  width and the row strides
+    of x and the weights are multiples of 8."""
+    code = _act_code(act)
+    xdt, dt, rows, width, dev, ldx = _x_16bit(x)
+    hidden, pg, ldg = _weight("gate_weight", gate_weight, width, xdt, dev)
+    pu, ldu = _matrix("up_weight", up_weight, (hidden, width), xdt, dev)
+    py, ldy = _matrix("y", y, (rows, hidden), xdt, dev)
+    pkg, ldkg = _maybe_matrix("gate", gate, (rows, hidden), xdt, dev)
+    pku, ldku = _maybe_matrix("up", up, (rows, hidden), xdt, dev)
+    _enqueue(lambda s: load().tsgemm_gated_linear(rows, hidden, width, dt, code, x.data_ptr(), ldx, pg, ldg, pu, ldu, py, ldy,
+                                                  pkg, ldkg, pku, ldku, s), stream, x)
+
+
+def gated_linear_grad(dy, x, gate_weight, up_weight, gate, up, dx=None, dgate_weight=None, dup_weight=None, act="silu",
+                      workspace=None, stream=None) -> None:
+    """tsgemm_gated_linear_grad: dx[rows, width], dgate_weight and
+    dup_weight[hidden, width] (None: not wanted; the weights' only together) from
+    dy[rows, hidden] and what gated_linear left in gate and up.  All are of x's
+    dtype.  `workspace`: a tensor for the projections' gradients
+    (gated_linear_grad_workspace bytes); by default torch's allocator gives one."""
+    code = _act_code(act)
+    xdt, dt, rows, width, dev, ldx = _x_16bit(x)
+    hidden, pg, ldg = _weight("gate_weight", gate_weight, width, xdt, dev)
+    pu, ldu = _matrix("up_weight", up_weight, (hidden, width), xdt, dev)
+    pdy, lddy = _matrix("dy", dy, (rows, hidden), xdt, dev)
+    pkg, ldkg = _matrix("gate", gate, (rows, hidden), xdt, dev)
+    pku, ldku = _matrix("up", up, (rows, hidden), xdt, dev)
+    pdx, lddx = _maybe_matrix("dx", dx, (rows, width), xdt, dev)
+    pdg, lddg = _maybe_matrix("dgate_weight", dgate_weight, (hidden, width), xdt, dev)
+    pdu, lddu = _maybe_matrix("dup_weight", dup_weight, (hidden, width), xdt, dev)
+    pw, have, keep = _workspace(gated_linear_grad_workspace(rows, hidden, width), workspace, x, stream)
+    _enqueue(lambda s: load().tsgemm_gated_linear_grad(rows, hidden, width, dt, code, pdy, lddy, x.data_ptr(), ldx, pg, ldg, pu, ldu,
+                                                       pkg, ldkg, pku, ldku, pdx, lddx, pdg, lddg, pdu, lddu, pw, have, s), stream, x)
+
+
+def gated_linear_grad_workspace(rows: int, hidden: int, width: int) -> int:
+    """Bytes of workspace a gated_linear_grad of this shape takes."""
+    return _check(load().tsgemm_gated_linear_grad_workspace(rows, hidden, width))
+
+
+def _index_vector(name, t, n, dev):
+    import torch
+    return _vector(name, t, n, torch.int64, dev)
+
+
+def linear_cross_entropy(x, weight, target, loss, lse, ignore_index=-100, workspace=None, stream=None) -> None:
+    """tsgemm_linear_cross_entropy: with the logits l = x @ weight^T, which are not
+    kept, lse[rows] = log(sum(exp(l))) and loss[rows] = lse - l[target], float32; 0
+    where target[rows] (int64) is ignore_index.  x[rows, width] and weight[vocab, width]
+    are float16 or bfloat16, their width and row strides multiples of 8.  `workspace`:
+    a tensor for the tiles' sums (linear_cross_entropy_workspace bytes); by default
+    torch's allocator gives one."""
+    import torch
+    xdt, dt, rows, width, dev, ldx = _x_16bit(x)
+    vocab, pwt, ldw = _weight("weight", weight, width, xdt, dev)
+    if target is None or loss is None or lse is None:
+        raise ValueError("target, loss and lse must be given")
+    pt = _index_vector("target", target, rows, dev)
+    pl = _vector("loss", loss, rows, torch.float32, dev)
+    ps = _vector("lse", lse, rows, torch.float32, dev)
+    pw, have, keep = _workspace(linear_cross_entropy_workspace(rows, vocab, width), workspace, x, stream)
+    _enqueue(lambda s: load().tsgemm_linear_cross_entropy(rows, vocab, width, dt, x.data_ptr(), ldx, pwt, ldw, pt, ignore_index, pl, ps,
+                                                          pw, have, s), stream, x)
+
+
+def linear_cross_entropy_workspace(rows: int, vocab: int, width: int) -> int:
+    """Bytes of workspace a linear_cross_entropy of this shape takes."""
+    return _check(load().tsgemm_linear_cross_entropy_workspace(rows, vocab, width))
+
+
+def linear_cross_entropy_grad(dloss, x, weight, target, lse, dx=None, dweight=None, ignore_index=-100, workspace=None, stream=None) -> None:
+    """tsgemm_linear_cross_entropy_grad: dx[rows, width] and dweight[vocab, width]
+    (None: not wanted), of x's dtype, from the gradient of every row's loss,
+    dloss[rows] (float32), and the lse that linear_cross_entropy wrote.  Rows whose
+    target is ignore_index count for nothing, whatever x holds there.  `workspace`: a
+    tensor for a piece of the logits' gradient
+    (linear_cross_entropy_grad_workspace bytes); by default torch's allocator gives one."""
+    import torch
+    xdt, dt, rows, width, dev, ldx = _x_16bit(x)
+    vocab, pwt, ldw = _weight("weight", weight, width, xdt, dev)
+    if dloss is None or target is None or lse is None:
+        raise ValueError("dloss, target and lse must be given")
+    pd = _vector("dloss", dloss, rows, torch.float32, dev)
+    pt = _index_vector("target", target, rows, dev)
+    ps = _vector("lse", lse, rows, torch.float32, dev)
+    pdx, lddx = _maybe_matrix("dx", dx, (rows, width), xdt, dev)
+    pdw, lddw = _maybe_matrix("dweight", dweight, (vocab, width), xdt, dev)
+    pw, have, keep = _workspace(linear_cross_entropy_grad_workspace(rows, vocab, width), workspace, x, stream)
+    _enqueue(lambda s: load().tsgemm_linear_cross_entropy_grad(rows, vocab, width, dt, pd, x.data_ptr(), ldx, pwt, ldw, pt, ignore_index,
+                                                               ps, pdx, lddx, pdw, lddw, pw, have, s), stream, x)
+
+
+def linear_cross_entropy_grad_workspace(rows: int, vocab: int, width: int) -> int:
+    """Bytes of workspace a linear_cross_entropy_grad of this shape takes."""
+    return _check(load().tsgemm_linear_cross_entropy_grad_workspace(rows, vocab, width))
 
 
 def worker_numbering(num_workgroups: int, num_xcds: int, num_active: int) -> np.ndarray:

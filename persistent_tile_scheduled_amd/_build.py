@@ -5,7 +5,9 @@ host code (tsgemm.hip), one unit per fp16/bf16 dtype and tile shape
 (tsgemm_gemm_tu.hip with -DTSG_TU_*), the block-scaled FP8 unit
 (tsgemm_mx_tu.hip), and the operators around it: their host code
 (tsgemm_ops.hip), the row operators (tsgemm_rows_tu.hip) and the weight
-gradient (tsgemm_wgrad_tu.hip).  The objects are linked into one shared library.
+gradient (tsgemm_wgrad_tu.hip); the gated projection and the linear head's cross
+entropy: their host code (tsgemm_linear.hip) and one unit per type
+(tsgemm_linear_tu.hip with -DTSG_LIN_DT).  The objects are linked into one shared library.
 Beside it lies the binding's extension module (tsgemm_torch.cpp, g++ and torch's
 headers), which holds no kernel.
 """
@@ -35,7 +37,8 @@ FLAGS = [
 GEMM_TUS = [(dt, bm, bk) for dt in (1, 2) for bm in (128, 256) for bk in (32, 64)]
 UNITS = ([("tsgemm.hip", [], "host.o"), ("tsgemm_mx_tu.hip", [], "mx.o"),
           ("tsgemm_ops.hip", [], "ops.o"), ("tsgemm_rows_tu.hip", [], "rows.o"),
-          ("tsgemm_wgrad_tu.hip", [], "wgrad.o")] +
+          ("tsgemm_wgrad_tu.hip", [], "wgrad.o"), ("tsgemm_linear.hip", [], "linear.o")] +
+         [("tsgemm_linear_tu.hip", [f"-DTSG_LIN_DT={dt}"], f"linear_{dt}.o") for dt in (1, 2)] +
          [("tsgemm_gemm_tu.hip", [f"-DTSG_TU_DT={dt}", f"-DTSG_TU_BM={bm}", f"-DTSG_TU_BK={bk}"],
            f"gemm_{dt}_{bm}_{bk}.o") for dt, bm, bk in GEMM_TUS])
 

@@ -1,0 +1,62 @@
+// The rules that choose tiles, splits of the sum and pieces of the vocabulary for
+// the products of tsgemm_linear_kernel.h: plain C++, for the launches and for
+// tests that ask which kernel a shape takes.
+#pragma once
+
+#include <stdint.h>
+
+#include <initializer_list>
+
+namespace tsg {
+
+struct LinShape {
+    int tile;
+    int64_t m_blocks, n_blocks, slabs, splits, per_split;
+};
+
+// Tile edge (and, where the product may be split along its sum, the splits) by the
+// time they should take, in us: rounds of workgroups (one 256 x 256 tile or two 128
+// x 128 tiles per compute unit) times the slabs of one and a start, plus the
+// splits' fp32 products written and read and a second launch.
+// `columns`: of the product per tile edge T, T or (two projections) T / 2.
+inline LinShape linear_shape(int64_t M, int64_t N, int64_t slabs, bool halves, bool may_split) {
+    constexpr int64_t kCus = 256;  // MI355X
+    LinShape best = {};
+    double best_us = 0;
+    for (int tile : {256, 128}) {
+        const int64_t cols = halves ? tile / 2 : tile;
+        const int64_t mb = (M + tile - 1) / tile, nb = (N + cols - 1) / cols, tiles = mb * nb, room = tile == 256 ? kCus : 2 * kCus;
+        for (int64_t splits = 1, per = slabs; splits <= 64; splits = (slabs + per - 2) / (per - 1)) {
+            per = (slabs + splits - 1) / splits;
+            if (splits > 1 && tiles * splits > 2 * room) break;
+            const double slab_us = tile == 256 ? 1.2 : tiles * splits <= kCus ? 0.45 : 0.8;
+            const double rounds = (double)((tiles * splits + room - 1) / room);
+            const double product = 8e-6 * (double)(M * N) / 4.0 + 0.03;
+            const double us = rounds * ((double)per * slab_us + 3.0) + (splits > 1 ? 3.0 + (double)splits * product : 0.0);
+            if (best.tile == 0 || us < best_us) {
+                best = {tile, mb, nb, slabs, splits, per};
+                best_us = us;
+            }
+            if (!may_split || per <= 1) break;
+        }
+    }
+    return best;
+}
+
+inline int64_t round_up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
+
+// Columns of a gradient's halves dg and du: whole tiles.
+inline int64_t gated_pitch(int64_t hidden) { return round_up(hidden, 256); }
+
+// Columns of the vocabulary that the gradient of the logits is held for at a time:
+// whole tiles, all of them if their 16-bit values take at most 512 MiB, never below
+// 2048, nor past 2^22 (32-bit offsets in a quarter of a slab).
+inline int64_t vocab_piece(int64_t rows, int64_t vocab) {
+    const int64_t most = (int64_t(1) << 28) / (rows > 0 ? rows : 1) / 256 * 256;
+    const int64_t all = round_up(vocab, 256), piece = most < 2048 ? 2048 : most < (1 << 22) ? most : 1 << 22;
+    if (all <= piece) return all;
+    const int64_t pieces = (all + piece - 1) / piece;
+    return round_up((vocab + pieces - 1) / pieces, 256);
+}
+
+}  // namespace tsg

@@ -1,0 +1,97 @@
+// The launches of one type's kernels (-DTSG_LIN_DT=1: fp16, 2: bf16).
+#include "tsgemm_linear_kernel.h"
+#include "tsgemm_linear_launch.h"
+#include "tsgemm_linear_rows.h"
+
+namespace tsg {
+
+namespace {
+
+constexpr int DT = TSG_LIN_DT;
+
+template <int AL, int BL, int EPI>
+void product_of(int tile, const LinArgs& a, hipStream_t s) {
+    const dim3 grid(a.m_blocks * a.n_blocks * a.splits), block(256);
+    if (tile == 256) hipLaunchKernelGGL((linear_kernel<DT, AL, BL, EPI, 256>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((linear_kernel<DT, AL, BL, EPI, 128>), grid, block, 0, s, a);
+}
+
+}  // namespace
+
+template <>
+void LinearOf<DT>::product(LinKind kind, int tile, const LinArgs& a, hipStream_t s) {
+    switch (kind) {
+        case LIN_KIND_GATED: return product_of<LIN_ALONG, LIN_ALONG, LIN_GATED>(tile, a, s);
+        case LIN_KIND_LSE: return product_of<LIN_ALONG, LIN_ALONG, LIN_LSE>(tile, a, s);
+        case LIN_KIND_DLOGITS: return product_of<LIN_ALONG, LIN_ALONG, LIN_DLOGITS>(tile, a, s);
+        case LIN_KIND_DX: return product_of<LIN_ALONG, LIN_ACROSS, LIN_OUT>(tile, a, s);
+        case LIN_KIND_DW: return product_of<LIN_ACROSS, LIN_ACROSS, LIN_OUT>(tile, a, s);
+    }
+}
+
+template <>
+void LinearOf<DT>::sum(const LinSumArgs& a, hipStream_t s) {
+    const uint64_t count = (uint64_t)a.M * a.N / 8u;
+    hipLaunchKernelGGL(linear_sum_kernel<DT>, dim3((unsigned)((count + 255u) / 256u)), dim3(256), 0, s, a);
+}
+
+template <>
+void LinearOf<DT>::gated_slope(const GatedGradArgs& a, hipStream_t s) {
+    const uint64_t groups = (uint64_t)a.rows * ((a.filled / 8u + 255u) / 256u);
+    hipLaunchKernelGGL(gated_slope_kernel<DT>, dim3((unsigned)(groups < 4096u ? groups : 4096u)), dim3(256), 0, s, a);
+}
+
+template <>
+void LinearOf<DT>::loss_rows(const LossGradArgs& a, hipStream_t s) {
+    hipLaunchKernelGGL(loss_rows_kernel<DT>, dim3((unsigned)(a.rows < 1024 ? a.rows : 1024)), dim3(256), 0, s, a);
+}
+
+#if TSG_LIN_DT == 1  // what no type goes by
+// 16 rows a workgroup, 16 threads a row: sum of 2^e s over the parts, each
+// thread's over every 16th part in order, then over the threads in order.
+__global__ __launch_bounds__(256) void loss_join_kernel(LossArgs a) {
+    __shared__ float tops[16][16], sums[16][16];
+    const uint32_t i = threadIdx.x & 15u, j = threadIdx.x >> 4;
+    const int64_t r = (int64_t)blockIdx.x * 16 + i;
+    const auto zero_if_none = [](float e) { return e == -__builtin_inff() ? 0.0f : e; };
+    float top = -__builtin_inff(), sum = 0.0f;
+    if (r < a.rows) {
+        for (uint32_t p = j; p < a.parts; p += 16u) {
+            const float2 v = a.part[(size_t)p * a.rows + r];
+            const float t = fmaxf(top, v.x), from = zero_if_none(t);
+            sum = sum * __builtin_amdgcn_exp2f(top - from) + v.y * __builtin_amdgcn_exp2f(v.x - from);
+            top = t;
+        }
+    }
+    tops[j][i] = top;
+    sums[j][i] = sum;
+    __syncthreads();
+    if (j != 0u || r >= a.rows) return;
+    for (int k = 1; k < 16; ++k) top = fmaxf(top, tops[k][i]);
+    const float from = zero_if_none(top);
+    sum = 0.0f;
+    for (int k = 0; k < 16; ++k) sum += sums[k][i] * __builtin_amdgcn_exp2f(tops[k][i] - from);
+    // in fp64, divided by what the logits were multiplied with: the loss is the
+    // difference of two numbers that may be close
+    const double lse = (double)from / (double)kLog2e + log((double)sum);
+    a.lse[r] = (float)lse;
+    const int64_t t = a.target[r];
+    a.loss[r] = t == a.ignore ? 0.0f : t >= 0 && t < (int64_t)a.vocab ? (float)(lse - (double)a.hit[r]) : __builtin_nanf("");
+}
+
+// dweight = 0 of a call without rows
+__global__ __launch_bounds__(256) void linear_zero_kernel(uint16_t* out, int64_t ld, int64_t rows, uint32_t width) {
+    for (int64_t r = blockIdx.x; r < rows; r += gridDim.x)
+        for (uint32_t n = threadIdx.x * 8u; n < width; n += 2048u) *(u32x4*)(out + r * ld + n) = u32x4{0, 0, 0, 0};
+}
+
+void launch_loss_join(const LossArgs& a, hipStream_t s) {
+    hipLaunchKernelGGL(loss_join_kernel, dim3((unsigned)((a.rows + 15) / 16)), dim3(256), 0, s, a);
+}
+
+void launch_linear_zero(uint16_t* out, int64_t ld, int64_t rows, uint32_t width, hipStream_t s) {
+    hipLaunchKernelGGL(linear_zero_kernel, dim3((unsigned)(rows < 4096 ? rows : 4096)), dim3(256), 0, s, out, ld, rows, width);
+}
+#endif
+
+}  // namespace tsg
