@@ -371,7 +371,6 @@ int tsgemm_linear_cross_entropy_grad(int64_t rows, int64_t vocab, int64_t width,
     (void)hipGetLastError();
     of_type(dtype, [&](auto k) { k.loss_rows(g, s); });
     rc = launched("linear cross entropy gradient");
-    const float* const unscale = dtype == TSGEMM_FP16 ? g.unscale : nullptr;
     for (int64_t first = 0; first < vocab && rc == TSGEMM_OK; first += plan.piece) {
         const int64_t columns = vocab - first < plan.piece ? vocab - first : plan.piece;
         const bool last = first + plan.piece >= vocab, several = vocab > plan.piece;
@@ -385,7 +384,7 @@ int tsgemm_linear_cross_entropy_grad(int64_t rows, int64_t vocab, int64_t width,
             LinArgs a = product(plan.dx, rows, width);
             a.a = dl; a.lda = plan.piece; a.Ka = (uint32_t)plan.piece;
             a.b = wp; a.ldb = ldw; a.Kb = (uint32_t)columns;
-            a.out = out_dx; a.ldo = lddx; a.out_rows = (uint32_t)rows; a.unscale = unscale;
+            a.out = out_dx; a.ldo = lddx; a.out_rows = (uint32_t)rows; a.unscale = g.unscale;
             if (plan.dx.splits > 1 || several) a.sums = reinterpret_cast<float*>(w + plan.dx_sums);
             a.add = first > 0;
             of_type(dtype, [&](auto k) {
@@ -397,7 +396,7 @@ int tsgemm_linear_cross_entropy_grad(int64_t rows, int64_t vocab, int64_t width,
         if (rc == TSGEMM_OK && dweight) {
             LinArgs a = product(plan.dw, plan.piece, width);
             a.a = dl; a.lda = plan.piece; a.b = g.counted_x; a.ldb = width; a.Ka = a.Kb = (uint32_t)rows;
-            a.out = out_dw + first * lddw; a.ldo = lddw; a.out_rows = (uint32_t)columns; a.unscale = unscale;
+            a.out = out_dw + first * lddw; a.ldo = lddw; a.out_rows = (uint32_t)columns; a.unscale = g.unscale;
             if (plan.dw.splits > 1) a.sums = reinterpret_cast<float*>(w + plan.dw_sums);
             of_type(dtype, [&](auto k) {
                 k.product(LIN_KIND_DW, plan.dw.tile, a, s);

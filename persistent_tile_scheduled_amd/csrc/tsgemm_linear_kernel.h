@@ -77,7 +77,7 @@ struct LinArgs {
     const float* unscale;  // NULL: 1
 };
 
-template <int AL, int BL, int T>
+template <int T>
 struct LinTraits {
     static constexpr int BK = 64;
     static constexpr int WT = T / 2, F = WT / 16;     // a wave's share of either side, in values and in 16-wide blocks
@@ -85,11 +85,61 @@ struct LinTraits {
     static constexpr int ND = STAGE / 4096;           // DMAs of a wave per operand and slab
 };
 
-__device__ __forceinline__ float act_of(int act, float g) {
-    if (act == 1) return g / (1.0f + __expf(-g));
-    if (act == 2) return 0.5f * g * erfcf(-0.70710678f * g);
-    const float z = 0.79788456f * (g + 0.044715f * g * g * g);
-    return g / (1.0f + __expf(-2.0f * z));  // (1 + tanh z) / 2 is the logistic function of 2 z
+// Race-detection build (TSG_STRESS): a pause of 0 to ~2048 cycles of which every
+// wave draws its own sequence; one asm block, since code that the compiler sees
+// would take the registers that the accumulators need.  The count only falls, so
+// the loop ends.
+__device__ __forceinline__ uint32_t pause_seed(uint32_t wave) { return (blockIdx.x * 4u + wave + 1u) * 0x9E3779B1u; }
+__device__ __forceinline__ void lin_pause(uint32_t& state) {
+#if TSG_STRESS
+    uint32_t count;  // 0, 0, 0, 1, 2, 4, 8 or 16 times 128 cycles
+    asm volatile(
+        "s_mul_i32 %0, %0, 0x19660d\n\ts_add_u32 %0, %0, 0x3c6ef35f\n\t"
+        "s_lshr_b32 %1, %0, 29\n\ts_lshl_b32 %1, 1, %1\n\ts_lshr_b32 %1, %1, 3\n"
+        ".Lpause%=:\n\ts_cmp_eq_u32 %1, 0\n\ts_cbranch_scc1 .Lon%=\n\ts_sleep 2\n\ts_sub_u32 %1, %1, 1\n\t"
+        "s_branch .Lpause%=\n.Lon%=:"
+        : "+s"(state), "=&s"(count)::"scc", "memory");
+#else
+    (void)state;
+#endif
+}
+
+// The activations are g p(g), with p the logistic function of z = g (c + k g^2)
+// (silu: c = 1, k = 0; gelu by tanh: (1 + tanh(z / 2)) / 2 is the logistic function of
+// z) or, BELL, the normal distribution function (gelu).  Both without a branch: an
+// accumulator that lives across one is copied.
+struct Act {
+    float c, k;  // times log2 e
+    __device__ __forceinline__ explicit Act(int act)
+        : c(act == 1 ? kLog2e : 1.5957691f * kLog2e), k(act == 1 ? 0.0f : 1.5957691f * 0.044715f * kLog2e) {}
+};
+constexpr int kActBell = 2;  // TSGEMM_GELU
+
+// The normal distribution function below -a, over exp(-a^2 / 2), a >= 0: a polynomial
+// in 1 / (1 + 0.3 a) fitted by least squares to the relative error, which is below
+// 4.3e-7 in fp32 for a up to 14, where exp(-a^2 / 2) ends.
+__device__ __forceinline__ float tail_over_bell(float a) {
+    const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.3f, a, 1.0f));
+    float h = 0.03622337058186531f;
+    h = __builtin_fmaf(h, t, -0.1593545526266098f);
+    h = __builtin_fmaf(h, t, 0.20981964468955994f);
+    h = __builtin_fmaf(h, t, -0.05664501339197159f);
+    h = __builtin_fmaf(h, t, 0.13000500202178955f);
+    h = __builtin_fmaf(h, t, 0.09951350837945938f);
+    h = __builtin_fmaf(h, t, 0.12081217765808105f);
+    h = __builtin_fmaf(h, t, 0.11962586641311646f);
+    return h * t;
+}
+// p(g); `bell` receives exp(-g^2 / 2) (BELL)
+template <bool BELL>
+__device__ __forceinline__ float act_share(const Act& k, float g, float& bell) {
+    if constexpr (BELL) {
+        bell = __builtin_amdgcn_exp2f(g * g * (-0.5f * kLog2e));
+        const float tail = bell * tail_over_bell(fabsf(g));
+        return g < 0.0f ? tail : 1.0f - tail;
+    } else {
+        return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-g * __builtin_fmaf(k.k, g * g, k.c)));
+    }
 }
 
 // Two values -> one dword of two 16-bit values (low half = a), round to nearest even.
@@ -134,21 +184,32 @@ __device__ __forceinline__ LinUnit lin_unit(const LinArgs& args, uint32_t unit) 
     return u;
 }
 
+// acc = a * b, in the registers that acc is in: with an output of its own the
+// accumulator of a tile's first slab could be another register than that of the
+// others, and the copies between them would lie right beside MFMAs that the compiler
+// does not see.
+template <int DT>
+__device__ __forceinline__ void mfma_first(f32x4& acc, i16x8 a, i16x8 b) {
+    if constexpr (DT == DT_FP16)
+        asm volatile("v_mfma_f32_16x16x32_f16 %0, %1, %2, 0" : "+a"(acc) : "v"(a), "v"(b));
+    else
+        asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, 0" : "+a"(acc) : "v"(a), "v"(b));
+}
+
 template <int DT, int AL, int BL, int EPI, int T>
 __global__ __launch_bounds__(256, T == 256 ? 1 : 2) void linear_kernel(LinArgs args) {
-    using TR = LinTraits<AL, BL, T>;
-    constexpr int F = TR::F, ND = TR::ND, WT = TR::WT, BK = TR::BK;
-    __shared__ __attribute__((aligned(1024))) uint8_t smem[2 * TR::STAGE];
+    using TR = LinTraits<T>;
+    constexpr int F = TR::F, ND = TR::ND, NL = 2 * ND, WT = TR::WT, BK = TR::BK, STAGE = TR::STAGE;
+    constexpr bool A_ALONG = AL == LIN_ALONG, B_ALONG = BL == LIN_ALONG;
+    __shared__ __attribute__((aligned(1024))) uint8_t smem[4 * STAGE];  // stage 0: A, B; stage 1: A, B
     typedef __attribute__((address_space(3))) uint8_t lds_u8;
     typedef __attribute__((address_space(3))) u32x4 lds_u32x4;
     const uint32_t lds_base = (uint32_t)reinterpret_cast<uintptr_t>((lds_u8*)smem);
     const uint32_t lane = threadIdx.x & 63u, l16 = lane & 15u, lg = lane >> 4;
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const uint32_t wr = wave >> 1, wc = wave & 1u;
-
-    const uint32_t units = args.m_blocks * args.n_blocks * args.splits;
-    const LinUnit u = lin_unit(args, worker_of_workgroup(blockIdx.x, units, 8u, units));
-    const uint32_t m0 = u.m_idx * T, n0 = u.n_idx * (EPI == LIN_GATED ? WT : T);  // a gated tile holds T/2 columns of each projection
+    uint32_t pauses = pause_seed(wave);  // race-detection build only
+    auto pause = [&]() __attribute__((always_inline)) { lin_pause(pauses); };
 
     // ---- sources.  A wave fetches a quarter of a slab's rows: T/4 rows along the
     // sum, or 16 across it.  Its descriptor starts there and ends with the matrix.
@@ -157,114 +218,274 @@ __global__ __launch_bounds__(256, T == 256 ? 1 : 2) void linear_kernel(LinArgs a
     // product to one lane: place 16 b + i of 32 holds row 8 (i / 4) + 4 b + i % 4.
     // A gated tile's rows alternate between the weights by waves. ----
     const uint32_t k_chunk = (lane & 7u) ^ (lane >> 3);
-    const int64_t ldb = EPI == LIN_GATED && (wave & 1u) ? args.ldb2 : args.ldb;
-    uint32_t voff_a[ND], voff_b[ND];
+    const uint32_t lda = (uint32_t)args.lda, ldb = (uint32_t)(EPI == LIN_GATED && (wave & 1u) ? args.ldb2 : args.ldb);
+    uint32_t voff[NL];
 #pragma unroll
     for (int q = 0; q < ND; ++q) {
-        if constexpr (AL == LIN_ALONG) {
-            voff_a[q] = (8u * q + lane / 8u) * (uint32_t)args.lda * 2u + k_chunk * 16u;
-        } else {
-            const uint32_t p = (wave * ND + q) * 64u + lane, r = p / (T / 8);
-            voff_a[q] = (r & 15u) * (uint32_t)args.lda * 2u + ((p % (T / 8)) ^ swz_b(r)) * 16u;
-        }
-        if constexpr (BL == LIN_ALONG) {
-            const uint32_t p = 8u * q + lane / 8u;
-            voff_b[q] = ((p & ~31u) + 8u * ((p >> 2) & 3u) + 4u * ((p >> 4) & 1u) + (p & 3u)) * (uint32_t)ldb * 2u + k_chunk * 16u;
-        } else {
-            const uint32_t p = (wave * ND + q) * 64u + lane, r = p / (T / 8);
-            voff_b[q] = (r & 15u) * (uint32_t)ldb * 2u + ((p % (T / 8)) ^ swz_b(r)) * 16u;
-        }
+        const uint32_t along = 8u * q + lane / 8u;
+        const uint32_t at = (wave * ND + q) * 64u + lane, across = at / (T / 8), chunk = (at % (T / 8)) ^ swz_b(across);
+        voff[q] = A_ALONG ? along * lda * 2u + k_chunk * 16u : (across & 15u) * lda * 2u + chunk * 16u;
+        voff[ND + q] = B_ALONG ? ((along & ~31u) + 8u * ((along >> 2) & 3u) + 4u * ((along >> 4) & 1u) + (along & 3u)) * ldb * 2u + k_chunk * 16u
+                               : (across & 15u) * ldb * 2u + chunk * 16u;
     }
-    // one operand's descriptor for a slab that starts at k0: `first` row or column of the tile
-    auto source = [&](auto along_c, const uint16_t* base, int64_t ld, uint32_t first, uint32_t end, uint32_t K, uint32_t k0) __attribute__((always_inline)) -> i32x4 {
+    // one operand's descriptor for a slab that starts at k0; `first`: the tile's row or column
+    auto source = [&](auto along_c, const uint16_t* base, int64_t ld, uint32_t first, uint32_t end, uint32_t K, uint32_t k0,
+                      uint32_t& dec) __attribute__((always_inline)) -> i32x4 {
         if constexpr (decltype(along_c)::value) {
             const uint32_t left = first < end ? end - first : 0u, rows = left < T / 4 ? left : T / 4;
             const uint32_t bytes = rows == 0u ? 0u : ((rows - 1u) * (uint32_t)ld + (K - k0)) * 2u;
+            dec = rows == 0u ? 0u : BK * 2u;
             return rsrc_words_u64(reinterpret_cast<uint64_t>(base) + ((uint64_t)first * (uint64_t)ld + k0) * 2u, bytes);
         } else {
             const uint32_t k = k0 + wave * 16u, left = k < K ? K - k : 0u, rows = left < 16u ? left : 16u;
             const uint32_t bytes = rows == 0u ? 0u : ((rows - 1u) * (uint32_t)ld + (end - first)) * 2u;
+            dec = 0u;
             return rsrc_words_u64(reinterpret_cast<uint64_t>(base) + ((uint64_t)k * (uint64_t)ld + first) * 2u, bytes);
         }
     };
-    using TRUE_ = std::integral_constant<bool, true>;
-    using FALSE_ = std::integral_constant<bool, false>;
-    auto fetch = [&](uint32_t slab) __attribute__((always_inline)) {
-        const bool second = slab >= args.seg_slabs;
-        const uint32_t k0 = (slab - (second ? args.seg_slabs : 0u)) * BK;
-        i32x4 ra, rb;
-        const uint16_t* a = EPI == LIN_OUT && second ? args.a2 : args.a;
-        if constexpr (AL == LIN_ALONG) ra = source(TRUE_{}, a, args.lda, m0 + wave * (T / 4), args.M, args.Ka, k0);
-        else ra = source(FALSE_{}, a, args.lda, m0, args.M, args.Ka, k0);
+
+    // ---- loader: its own walk over the workgroup's units, two slabs ahead of the
+    // MFMAs and on to the next unit's.  From slab to slab it steps the descriptors;
+    // at an event (the sum's second half, its last slab when that is not whole, the
+    // next unit) it forms them anew.  Past the last unit nothing is covered: the DMAs
+    // then write zeros that nobody reads, so that every slab issues the same. ----
+    const uint32_t units = args.m_blocks * args.n_blocks * args.splits, workers = gridDim.x;
+    const uint32_t first_unit = worker_of_workgroup(blockIdx.x, workers, 8u, workers);
+    uint32_t ld_unit = first_unit, ld_slab = 0, ld_end = 0, ld_event = 0, ld_m = 0, ld_n = 0;
+    uint32_t a_dec = 0, b_dec = 0;
+    i32x4 ra, rb;
+    auto seek = [&]() __attribute__((always_inline)) {
+        if (ld_slab == ld_end && ld_unit < units) {
+            const LinUnit u = lin_unit(args, ld_unit);
+            ld_unit += workers;
+            ld_slab = u.slab0;
+            ld_end = u.slab0 + u.slabs;
+            ld_m = u.m_idx * T;
+            ld_n = u.n_idx * (EPI == LIN_GATED ? WT : T);
+        }
+        const bool live = ld_slab != ld_end, second = EPI == LIN_OUT && ld_slab >= args.seg_slabs;
+        const uint32_t seg = second ? args.seg_slabs : 0u, k0 = (ld_slab - seg) * BK;
+        ra = source(std::integral_constant<bool, A_ALONG>{}, second ? args.a2 : args.a, args.lda, A_ALONG ? ld_m + wave * (T / 4) : ld_m,
+                    args.M, args.Ka, k0, a_dec);
         if constexpr (EPI == LIN_GATED)
-            rb = source(TRUE_{}, (wave & 1u) ? args.b2 : args.b, ldb, n0 + (wave >> 1) * (T / 4), args.N, args.Kb, k0);
-        else if constexpr (BL == LIN_ALONG) rb = source(TRUE_{}, args.b, ldb, n0 + wave * (T / 4), args.N, args.Kb, k0);
-        else rb = source(FALSE_{}, second ? args.b2 : args.b, second ? args.ldb2 : args.ldb, n0, args.N, args.Kb, k0);
-        const uint32_t past = k0 + k_chunk * 8u >= args.Ka ? 0x80000000u : 0u;
-        asm volatile("s_nop 4" ::: "memory");  // a vector write of a descriptor -> its use
-        static_for<0, ND>([&](auto q_c) __attribute__((always_inline)) {
-            constexpr int q = decltype(q_c)::value;
-            dma16_at<q * 1024u>(lds_base + wave * ND * 1024u, AL == LIN_ALONG ? voff_a[q] | past : voff_a[q], ra);
-        });
-        static_for<0, ND>([&](auto q_c) __attribute__((always_inline)) {
-            constexpr int q = decltype(q_c)::value;
-            dma16_at<TR::STAGE + q * 1024u>(lds_base + wave * ND * 1024u, BL == LIN_ALONG ? voff_b[q] | past : voff_b[q], rb);
-        });
+            rb = source(std::integral_constant<bool, true>{}, (wave & 1u) ? args.b2 : args.b, ldb, ld_n + (wave >> 1) * (T / 4), args.N, args.Kb, k0, b_dec);
+        else
+            rb = source(std::integral_constant<bool, B_ALONG>{}, second ? args.b2 : args.b, second ? args.ldb2 : args.ldb,
+                        B_ALONG ? ld_n + wave * (T / 4) : ld_n, args.N, args.Kb, k0, b_dec);
+        const uint32_t K = args.Ka < args.Kb ? args.Ka : args.Kb;
+        const uint32_t whole = K / BK, run = seg + (k0 / BK < whole ? whole : k0 / BK + 1u);
+        ld_event = run < ld_end ? run : ld_end;
+        if (!live) {
+            ra.z = rb.z = 0;
+            a_dec = b_dec = 0u;
+            ld_event = 0xFFFFFFFFu;
+        }
+        if constexpr (A_ALONG || B_ALONG) {
+            const uint32_t past = k0 + k_chunk * 8u >= K ? 0x80000000u : 0u;
+#pragma unroll
+            for (int q = 0; q < NL; ++q)
+                if (q < ND ? A_ALONG : B_ALONG) voff[q] = (voff[q] & 0x7FFFFFFFu) | past;
+        }
+        asm volatile("s_nop 4" : "+s"(ra), "+s"(rb)::"memory");  // a vector write of a descriptor -> its use
+    };
+    const uint32_t dma_first = lds_base + wave * ND * 1024u;
+    uint32_t dma_lds = dma_first;
+    const uint64_t a_step = A_ALONG ? BK * 2u : (uint64_t)BK * lda * 2u, b_step = B_ALONG ? BK * 2u : (uint64_t)BK * ldb * 2u;
+    auto add64 = [](i32x4& r, uint64_t d) __attribute__((always_inline)) {
+        const uint64_t a = (((uint64_t)(uint32_t)r.y) << 32 | (uint32_t)r.x) + d;  // stride bits are 0
+        r.x = (int)(uint32_t)a;
+        r.y = (int)(uint32_t)(a >> 32);
+    };
+    // One step in four pieces, for four gaps between MFMAs; each is pinned there by
+    // the empty asm around it.
+    constexpr int PIECES = 4;
+    auto step = [&](auto p_c) __attribute__((always_inline)) {
+        constexpr int p = decltype(p_c)::value;
+        if constexpr (p == 0) {
+            asm volatile("" : "+s"(ra));
+            add64(ra, a_step);
+            if constexpr (A_ALONG) ra.z -= (int)a_dec;
+            asm volatile("" : "+s"(ra));
+        } else if constexpr (p == 1) {
+            asm volatile("" : "+s"(rb));
+            add64(rb, b_step);
+            if constexpr (B_ALONG) rb.z -= (int)b_dec;
+            asm volatile("" : "+s"(rb));
+        } else if constexpr (p == 2) {
+            asm volatile("" : "+s"(dma_lds));
+            dma_lds = dma_lds == dma_first ? dma_first + 2 * STAGE : dma_first;
+            asm volatile("" : "+s"(dma_lds));
+        } else {
+            asm volatile("" : "+s"(ld_slab));
+            if (__builtin_expect(++ld_slab == ld_event, 0)) seek();
+            asm volatile("" : "+s"(ld_slab), "+s"(ra), "+s"(rb));
+        }
+    };
+    // M0 for a DMA is written a gap before it
+    auto m0_op = [&](auto q_c) __attribute__((always_inline)) {
+        constexpr int q = decltype(q_c)::value;
+        set_m0<q < ND ? q * 1024u : (uint32_t)STAGE + (q - ND) * 1024u>(dma_lds);
+    };
+    auto dma_op = [&](auto q_c) __attribute__((always_inline)) {
+        constexpr int q = decltype(q_c)::value;
+        pause();
+        if constexpr (q < ND) dma16_m0(voff[q], ra);
+        else dma16_m0(voff[q], rb);
+    };
+    auto dma_now = [&](auto q_c) __attribute__((always_inline)) {
+        constexpr int q = decltype(q_c)::value;
+        if constexpr (q < ND) dma16_at<q * 1024u>(dma_lds, voff[q], ra);
+        else dma16_at<(uint32_t)STAGE + (q - ND) * 1024u>(dma_lds, voff[q], rb);
     };
 
     // ---- fragments.  Across the sum the columns of two 16-wide blocks are
     // interleaved: block b's lane group g holds 8 g + 4 (b ^ (g & 1)) + 0..3 of 32,
     // so that one read's 16 lanes spread over the banks. ----
-    i16x8 fa[F][2], fb[F][2];
-    auto read = [&](auto along_c, uint32_t base, uint32_t side, int f, int k) __attribute__((always_inline)) -> i16x8 {
+    constexpr int AA = A_ALONG ? 2 : F, AB = B_ALONG ? 2 : F;  // address registers: per k-step, or per block
+    uint32_t a_off[AA], b_off[AB], a_at[AA], b_at[AB];
+    auto offset = [&](bool along, uint32_t side, uint32_t i) __attribute__((always_inline)) -> uint32_t {
+        if (along) return (side * WT + l16) * 128u + ((i * 4u + lg) ^ (l16 & 7u)) * 16u;
+        const uint32_t r = 8u * lg + (l16 >> 2), chunk = (side * WT + 32u * (i / 2)) / 8u + (l16 & 3u);
+        return r * (T * 2) + (chunk ^ swz_b(r)) * 16u + 8u * ((i & 1u) ^ (l16 & 1u));
+    };
+#pragma unroll
+    for (int i = 0; i < AA; ++i) a_off[i] = lds_base + offset(A_ALONG, wr, i);
+#pragma unroll
+    for (int i = 0; i < AB; ++i) b_off[i] = lds_base + STAGE + offset(B_ALONG, wc, i);
+    i16x4 fa[F][2][2], fb[F][2][2];  // [block][k-step][half]
+    auto read = [&](auto along_c, i16x4 (&to)[2], const uint32_t* at, auto f_c, auto k_c) __attribute__((always_inline)) {
+        constexpr int f = decltype(f_c)::value, k = decltype(k_c)::value;
         if constexpr (decltype(along_c)::value) {
-            const uint32_t at = base + (side * WT + 16u * f + l16) * 128u + (((uint32_t)k * 4u + lg) ^ (l16 & 7u)) * 16u;
-            return __builtin_bit_cast(i16x8, *(const lds_u32x4*)(lds_u8*)(uintptr_t)at);
+            const i16x8 v = __builtin_bit_cast(i16x8, *(const lds_u32x4*)((lds_u8*)(uintptr_t)at[k] + f * 2048));
+            to[0] = __builtin_shufflevector(v, v, 0, 1, 2, 3);
+            to[1] = __builtin_shufflevector(v, v, 4, 5, 6, 7);
         } else {
-            const uint32_t r = 8u * lg + (l16 >> 2);
-            const uint32_t chunk = (side * WT + 32u * (f / 2)) / 8u + (l16 & 3u);
-            const uint32_t at = base + r * (T * 2) + (chunk ^ swz_b(r)) * 16u + 8u * ((f & 1u) ^ (l16 & 1u)) + k * 32u * (T * 2);
-            const i16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(lds_u8*)(uintptr_t)at);
-            const i16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(lds_u8*)(uintptr_t)(at + 4u * (T * 2)));
-            return __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
+            to[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)((lds_u8*)(uintptr_t)at[f] + k * 32 * (T * 2)));
+            to[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)((lds_u8*)(uintptr_t)at[f] + (k * 32 + 4) * (T * 2)));
         }
     };
+    // read i of F of half a side's blocks, both k-steps
+    auto read_a = [&](auto half_c, auto i_c) __attribute__((always_inline)) {
+        constexpr int f = decltype(half_c)::value * F / 2 + decltype(i_c)::value / 2, k = decltype(i_c)::value % 2;
+        read(std::integral_constant<bool, A_ALONG>{}, fa[f][k], a_at, std::integral_constant<int, f>{}, std::integral_constant<int, k>{});
+    };
+    auto read_b = [&](auto half_c, auto i_c) __attribute__((always_inline)) {
+        constexpr int f = decltype(half_c)::value * F / 2 + decltype(i_c)::value / 2, k = decltype(i_c)::value % 2;
+        read(std::integral_constant<bool, B_ALONG>{}, fb[f][k], b_at, std::integral_constant<int, f>{}, std::integral_constant<int, k>{});
+    };
+    auto address = [&](auto i_c, uint32_t stage) __attribute__((always_inline)) {
+        constexpr int i = decltype(i_c)::value;
+        if constexpr (i < AB) b_at[i] = b_off[i] + stage;
+        else a_at[i - AB] = a_off[i - AB] + stage;
+    };
 
+    // ---- a slab in two phases of F * F MFMAs.  Every pair of MFMAs adds the slab's two
+    // k-steps to one accumulator, the second taking it from the matrix core's
+    // forwarding path.  Phase 1 goes over the column blocks' first half, phase 2 over
+    // the second, rows of blocks in order in both, so that the fragments of both
+    // k-steps fit the registers:
+    //   phase 1 reads this slab's second halves of A and B while it uses the first;
+    //   phase 2 waits for the next slab and passes the workgroup's barrier, reads the
+    //   next slab's first half of B, and of A each row of blocks once it is used up, and
+    //   refills the stage that phase 1 read out (the last DMAs go out in phase 1).
+    // No register is refilled within kGap MFMAs of its last use: an MFMA may still be
+    // fetching it. ----
     f32x4 acc[F][F];
 #pragma unroll
     for (int fm = 0; fm < F; ++fm)
 #pragma unroll
-        for (int fn = 0; fn < F; ++fn) {
-            acc[fm][fn] = f32x4{0.f, 0.f, 0.f, 0.f};
-            asm volatile("" : "+a"(acc[fm][fn]));
+        for (int fn = 0; fn < F; ++fn) asm volatile("" : "=a"(acc[fm][fn]));
+    constexpr int STEPS = F * F, START = kGap > 2 ? kGap : 2;
+    constexpr int SPACE = T == 256 ? 4 : 1;                                   // MFMAs between DMAs
+    constexpr int DF = START + (NL - 1) * SPACE < STEPS ? NL : (STEPS - START + SPACE - 1) / SPACE;  // DMAs of phase 2
+    constexpr int LATE = DF < NL ? START + (NL - 1 - DF) * SPACE + 1 : 0;     // phase 1: gap after its DMAs
+    constexpr int STEP_AT = DF < NL ? LATE : START + (DF - 1) * SPACE + 1;    // the loader's step, in phase 1 or 2
+    static_assert(STEP_AT + PIECES <= STEPS, "the loader's step needs gaps");
+    constexpr auto refill = [](int i) constexpr {  // phase 2: gap of read i of A's first half
+        int gap = START + F;
+        for (int j = 0; j <= i; ++j) {
+            const int free = (j / 2) * F + F - 1 + kGap;
+            gap = gap > free ? gap : free;
+            if (j < i) ++gap;
         }
-    asm volatile("s_nop 1" ::: "memory");  // a vector write of a register -> an MFMA that reads it
-
-    for (uint32_t s = 0; s < u.slabs; ++s) {
-        lds_barrier();
-        fetch(u.slab0 + s);
-        wait_vm<0>();
-        lds_barrier();
-        static_for<0, 2>([&](auto k_c) __attribute__((always_inline)) {
-            constexpr int k = decltype(k_c)::value;
-#pragma unroll
-            for (int f = 0; f < F; ++f) {
-                fa[f][k] = read(std::integral_constant<bool, AL == LIN_ALONG>{}, lds_base, wr, f, k);
-                fb[f][k] = read(std::integral_constant<bool, BL == LIN_ALONG>{}, lds_base + TR::STAGE, wc, f, k);
+        return gap;
+    };
+    static_assert(refill(F - 1) < STEPS && START + 2 * F <= STEPS, "every read needs a gap");
+    using I0 = std::integral_constant<int, 0>;
+    using I1 = std::integral_constant<int, 1>;
+    using TRUE_ = std::integral_constant<bool, true>;
+    using FALSE_ = std::integral_constant<bool, false>;
+    uint32_t stage = 0;  // of the slab at hand: 0 or 2 * STAGE
+    auto phase = [&](auto second_c, auto clear_c) __attribute__((always_inline)) {
+        constexpr bool SECOND = decltype(second_c)::value, CLEAR = decltype(clear_c)::value;
+        constexpr int B_SPACE = T == 256 ? 2 : 1;
+        static_for<0, STEPS>([&](auto s_c) __attribute__((always_inline)) {
+            constexpr int s = decltype(s_c)::value, k = s % 2;
+            constexpr int fm = s / F, j = (s % F) / 2, fn = (SECOND ? F / 2 : 0) + ((fm & 1) ? F / 2 - 1 - j : j);
+            const i16x8 av = __builtin_shufflevector(fa[fm][k][0], fa[fm][k][1], 0, 1, 2, 3, 4, 5, 6, 7);
+            const i16x8 bv = __builtin_shufflevector(fb[fn][k][0], fb[fn][k][1], 0, 1, 2, 3, 4, 5, 6, 7);
+            if constexpr (CLEAR && k == 0) mfma_first<DT>(acc[fm][fn], bv, av);
+            else mfma16x16x32<DT>(acc[fm][fn], bv, av);
+            if constexpr (SECOND && s == 1) {
+                pause();
+                wait_vm<0>();   // the next slab has landed
+                lds_barrier();  // ... for every wave, and this one is read out
+                pause();
+                stage = stage == 0u ? 2u * STAGE : 0u;
             }
-            asm volatile("s_nop 1" ::: "memory");
-#pragma unroll
-            for (int fm = 0; fm < F; ++fm)
-#pragma unroll
-                for (int fn = 0; fn < F; ++fn) mfma16x16x32<DT>(acc[fm][fn], fb[fn][k], fa[fm][k]);
+            if constexpr (SECOND && s >= 2 && s < 4)  // the next slab's addresses
+                static_for<(AA + AB) * (s - 2) / 2, (AA + AB) * (s - 1) / 2>([&](auto i_c) __attribute__((always_inline)) { address(i_c, stage); });
+            if constexpr (s >= START) {
+                constexpr int i = s - START;
+                if constexpr (SECOND ? i % SPACE == 0 && i / SPACE < DF : i % SPACE == 0 && i / SPACE < NL - DF)
+                    dma_op(std::integral_constant<int, (SECOND ? 0 : DF) + i / SPACE>{});
+                if constexpr (SECOND) {
+                    if constexpr (i < F) read_b(I0{}, std::integral_constant<int, i>{});
+                    static_for<0, F>([&](auto r_c) __attribute__((always_inline)) {
+                        if constexpr (refill(decltype(r_c)::value) == s) read_a(I0{}, r_c);
+                    });
+                } else {
+                    if constexpr (i < F) read_a(I1{}, std::integral_constant<int, i>{});
+                    else if constexpr ((i - F) % B_SPACE == 0 && (i - F) / B_SPACE < F) read_b(I1{}, std::integral_constant<int, (i - F) / B_SPACE>{});
+                }
+            }
+            if constexpr (SECOND == (DF == NL) && s >= STEP_AT && s < STEP_AT + PIECES) step(std::integral_constant<int, s - STEP_AT>{});
+            if constexpr (s + 1 >= START) {
+                constexpr int i = s + 1 - START;
+                if constexpr (s + 1 < STEPS && i % SPACE == 0 && i / SPACE < (SECOND ? DF : NL - DF))
+                    m0_op(std::integral_constant<int, (SECOND ? 0 : DF) + i / SPACE>{});
+            }
+            __builtin_amdgcn_sched_barrier(0);
         });
+    };
+
+    // two slabs on their way (of the second what phase 2 would have issued), the first one's first halves read
+    auto advance = [&]() __attribute__((always_inline)) {
+        static_for<0, PIECES>([&](auto p_c) __attribute__((always_inline)) { step(p_c); });
+    };
+    seek();
+    static_for<0, NL>([&](auto q_c) __attribute__((always_inline)) { dma_now(q_c); });
+    advance();
+    static_for<0, DF>([&](auto q_c) __attribute__((always_inline)) { dma_now(q_c); });
+    if constexpr (DF == NL) advance();
+    pause();
+    wait_vm<DF>();
+    lds_barrier();
+    pause();
+    static_for<0, AA + AB>([&](auto i_c) __attribute__((always_inline)) { address(i_c, 0u); });
+    static_for<0, F>([&](auto i_c) __attribute__((always_inline)) { read_b(I0{}, i_c); });
+    static_for<0, F>([&](auto i_c) __attribute__((always_inline)) { read_a(I0{}, i_c); });
+
+    for (uint32_t unit = first_unit; unit < units; unit += workers) {
+    const LinUnit u = lin_unit(args, unit);
+    const uint32_t m0 = u.m_idx * T, n0 = u.n_idx * (EPI == LIN_GATED ? WT : T);  // a gated tile holds T/2 columns of each projection
+    phase(FALSE_{}, TRUE_{});
+    phase(TRUE_{}, TRUE_{});
+    for (uint32_t s = 1; s < u.slabs; ++s) {
+        phase(FALSE_{}, FALSE_{});
+        phase(TRUE_{}, FALSE_{});
     }
-    gap_nops();
-    wait_vm<0>();
-#pragma unroll
-    for (int fm = 0; fm < F; ++fm)
-#pragma unroll
-        for (int fn = 0; fn < F; ++fn) asm volatile("" : "+a"(acc[fm][fn]));  // not read before the gap above
+    gap_nops();  // the last MFMAs have written their accumulators
 
     // ---- where a lane's values belong: of block fm one row, of the pair t of
     // column blocks 8 consecutive columns ----
@@ -274,8 +495,16 @@ __global__ __launch_bounds__(256, T == 256 ? 1 : 2) void linear_kernel(LinArgs a
         return m0 + wr * WT + 32u * (fm / 2) + 8u * p + 4u * ((fm & 1u) ^ (p & 1u)) + (l16 & 3u);
     };
     const bool swap = BL == LIN_ACROSS && (lg & 1u) != 0u;
+    // Read in asm, where the values are used: read all at once, as the compiler would,
+    // they do not fit the registers beside the fragments of the next tile.
+    auto four = [&](const f32x4& from, float* v) __attribute__((always_inline)) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) asm volatile("v_accvgpr_read_b32 %0, %1" : "=v"(v[e]) : "a"(from[e]));
+    };
     auto eight = [&](int fm, int t, float* v) __attribute__((always_inline)) {
-        const f32x4 x = acc[fm][2 * t], y = acc[fm][2 * t + 1];
+        float x[4], y[4];
+        four(acc[fm][2 * t], x);
+        four(acc[fm][2 * t + 1], y);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             v[e] = swap ? y[e] : x[e];
@@ -285,24 +514,30 @@ __global__ __launch_bounds__(256, T == 256 ? 1 : 2) void linear_kernel(LinArgs a
     auto left = [](uint32_t at, uint32_t end) __attribute__((always_inline)) -> uint32_t { return at < end ? end - at : 0u; };
 
     if constexpr (EPI == LIN_GATED) {
+        const Act act(args.act);
+        auto gated = [&](auto bell_c) __attribute__((always_inline)) {
 #pragma unroll
-        for (int fm = 0; fm < F; ++fm) {
-            const uint32_t m = row_of(fm);
+            for (int fm = 0; fm < F; ++fm) {
+                const uint32_t m = row_of(fm);
 #pragma unroll
-            for (int t = 0; t < F / 4; ++t) {
-                float g[8], up[8], y[8];
-                eight(fm, t, g);
-                eight(fm, t + F / 4, up);
+                for (int t = 0; t < F / 4; ++t) {
+                    float g[8], up[8], y[8], bell;
+                    eight(fm, t, g);
+                    eight(fm, t + F / 4, up);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) y[e] = act_of(args.act, g[e]) * up[e];
-                const uint32_t n = n0 + wc * (WT / 2) + 32u * t + 8u * lg;
-                const uint32_t count = m < args.M ? left(n, args.N) : 0u;
-                if (count == 0u) continue;
-                store8<DT>(args.y + (int64_t)m * args.ldy + n, y, count);
-                if (args.gate) store8<DT>(args.gate + (int64_t)m * args.ldgate + n, g, count);
-                if (args.up) store8<DT>(args.up + (int64_t)m * args.ldup + n, up, count);
+                    for (int e = 0; e < 8; ++e) y[e] = g[e] * act_share<decltype(bell_c)::value>(act, g[e], bell) * up[e];
+                    const uint32_t n = n0 + wc * (WT / 2) + 32u * t + 8u * lg;
+                    const uint32_t count = m < args.M ? left(n, args.N) : 0u;
+                    if (count != 0u) {
+                        store8<DT>(args.y + (int64_t)m * args.ldy + n, y, count);
+                        if (args.gate) store8<DT>(args.gate + (int64_t)m * args.ldgate + n, g, count);
+                        if (args.up) store8<DT>(args.up + (int64_t)m * args.ldup + n, up, count);
+                    }
+                }
             }
-        }
+        };
+        if (args.act == kActBell) gated(TRUE_{});
+        else gated(FALSE_{});
     } else if constexpr (EPI == LIN_LSE) {
 #pragma unroll
         for (int fm = 0; fm < F; ++fm) {
@@ -383,6 +618,8 @@ __global__ __launch_bounds__(256, T == 256 ? 1 : 2) void linear_kernel(LinArgs a
             }
         }
     }
+    }
+    wait_vm<0>();  // no DMA may still target LDS when the workgroup retires
 }
 
 }  // namespace tsg

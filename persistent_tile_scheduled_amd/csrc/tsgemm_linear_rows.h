@@ -27,26 +27,24 @@ struct GatedGradArgs {
     int act;
 };
 
-// act(g) and its derivative.  All three are g p(g): with p the logistic function
-// of c g (1 + k g^2), or the normal distribution's.
-__device__ __forceinline__ void act_slope(int act, float g, float& value, float& slope) {
-    if (act == 2) {
-        const float p = 0.5f * erfcf(-0.70710678f * g);
-        value = g * p;
-        slope = p + g * 0.39894228f * __expf(-0.5f * g * g);
-        return;
-    }
-    const float c = act == 1 ? 1.0f : 1.5957691f, k = act == 1 ? 0.0f : 0.044715f;
-    const float z = c * g * (1.0f + k * g * g);
-    const float p = 1.0f / (1.0f + __expf(-z));
+// act(g) = g p(g) and its derivative p + g p'.
+template <bool BELL>
+__device__ __forceinline__ void act_slope(const Act& k, float g, float& value, float& slope) {
+    float bell;
+    const float p = act_share<BELL>(k, g, bell);
     value = g * p;
-    // p (1 - p) vanishes faster than g grows; past the range of exp it is 0, not 0 * inf
-    const float q = p * (1.0f - p) * c * (1.0f + 3.0f * k * g * g);
-    slope = p + (p == 0.0f || p == 1.0f ? 0.0f : g * q);
+    if constexpr (BELL) {
+        slope = __builtin_fmaf(g * 0.39894228f, bell, p);
+    } else {
+        // p (1 - p) z'; where p has run out of fp32 the slope is 0 or 1, not 0 * inf
+        const float rise = p * (1.0f - p) * __builtin_fmaf(3.0f * k.k, g * g, k.c) * (1.0f / kLog2e);
+        slope = p == 0.0f || p == 1.0f ? p : __builtin_fmaf(g, rise, p);
+    }
 }
 
-template <int DT>
+template <int DT, bool BELL>
 __global__ __launch_bounds__(256) void gated_slope_kernel(GatedGradArgs a) {
+    const Act act(a.act);
     const uint32_t chunks = a.filled / 8u;
     const uint32_t per_row = (chunks + 255u) / 256u;
     for (uint64_t w = blockIdx.x; w < (uint64_t)a.rows * per_row; w += gridDim.x) {
@@ -76,7 +74,7 @@ __global__ __launch_bounds__(256) void gated_slope_kernel(GatedGradArgs a) {
             const float d = unpack1<DT>((uint16_t)(wd[e / 2] >> (16 * (e % 2))));
             const float up = unpack1<DT>((uint16_t)(wu[e / 2] >> (16 * (e % 2))));
             float value, slope;
-            act_slope(a.act, unpack1<DT>((uint16_t)(wg[e / 2] >> (16 * (e % 2)))), value, slope);
+            act_slope<BELL>(act, unpack1<DT>((uint16_t)(wg[e / 2] >> (16 * (e % 2)))), value, slope);
             dg[e] = d * up * slope;
             du[e] = d * value;
             if (n + e >= a.hidden) dg[e] = du[e] = 0.0f;
@@ -108,15 +106,16 @@ struct LossGradArgs {
     const uint16_t* x;
     uint16_t* counted_x;  // [rows][width]: x, zero in rows that do not count; NULL: not wanted
     LossRow* row;
-    float* unscale;       // 1 / scale of dl
+    float* unscale;       // what dl is to be multiplied with
     int64_t ignore, rows, ldx;
     uint32_t width, vocab;
 };
 
-// What the gradient needs of every row.  fp16 has few exponents for dl, whose
-// values are a row's gradient times a probability: there dl is scaled by a power of
-// two that brings the largest |dloss| to [2^13, 2^14), so that fp16's least normal
-// value stands for 2^-27 of it.  Every workgroup finds that largest value for itself.
+// What the gradient needs of every row.  dl is held over the largest |dloss| of the
+// rows that count, so that of a loss's mean over the rows, all of whose dloss are
+// alike, no rounding of dloss itself enters; fp16, which has few exponents, holds 2^13
+// times that, and its least normal value stands for 2^-27 of the largest.  Every
+// workgroup finds that largest value for itself.
 template <int DT>
 __global__ __launch_bounds__(256) void loss_rows_kernel(LossGradArgs a) {
     __shared__ float most[4];
@@ -124,27 +123,22 @@ __global__ __launch_bounds__(256) void loss_rows_kernel(LossGradArgs a) {
         const int64_t t = a.target[r];
         return t != a.ignore && t >= 0 && t < (int64_t)a.vocab;
     };
-    float scale = 1.0f;
-    if constexpr (DT == DT_FP16) {
-        float top = 0.0f;
-        for (int64_t r = threadIdx.x; r < a.rows; r += 256)
-            if (counts(r)) top = fmaxf(top, fabsf(a.dloss[r]));
+    constexpr float kMore = DT == DT_FP16 ? 8192.0f : 1.0f;
+    float top = 0.0f;
+    for (int64_t r = threadIdx.x; r < a.rows; r += 256)
+        if (counts(r)) top = fmaxf(top, fabsf(a.dloss[r]));
 #pragma unroll
-        for (int d = 1; d < 64; d *= 2) top = fmaxf(top, __shfl_xor(top, d));
-        if ((threadIdx.x & 63u) == 0u) most[threadIdx.x >> 6] = top;
-        __syncthreads();
-        top = fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3]));
-        // exponent fields: 2^(13 - e) with e the largest value's exponent, held in fp32's range
-        const int e = (int)(__builtin_bit_cast(uint32_t, top) >> 23) - 127;
-        const int p = 13 - (e < -100 ? -100 : e);
-        if (top > 0.0f && e < 128) scale = __builtin_bit_cast(float, (uint32_t)(p + 127) << 23);
-        if (blockIdx.x == 0 && threadIdx.x == 0) *a.unscale = __builtin_bit_cast(float, (uint32_t)(127 - (top > 0.0f && e < 128 ? p : 0)) << 23);
-    }
+    for (int d = 1; d < 64; d *= 2) top = fmaxf(top, __shfl_xor(top, d));
+    if ((threadIdx.x & 63u) == 0u) most[threadIdx.x >> 6] = top;
+    __syncthreads();
+    top = fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3]));
+    if (!(top >= 0x1p-110f && top < __builtin_inff())) top = 1.0f;  // no scale comes of it
+    if (blockIdx.x == 0 && threadIdx.x == 0) *a.unscale = top / kMore;
     for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
         const bool is = counts(r);
         if (threadIdx.x == 0) {
             LossRow row = {0.0f, 0.0f, -1, 0};
-            if (is) row = {a.lse[r] * kLog2e, a.dloss[r] * scale, (int32_t)a.target[r], 0};
+            if (is) row = {a.lse[r] * kLog2e, a.dloss[r] / top * kMore, (int32_t)a.target[r], 0};
             a.row[r] = row;
         }
         if (a.counted_x)

@@ -8,10 +8,12 @@ namespace tsg {
 namespace {
 
 constexpr int DT = TSG_LIN_DT;
+constexpr uint32_t kCus = 256;  // MI355X
 
 template <int AL, int BL, int EPI>
 void product_of(int tile, const LinArgs& a, hipStream_t s) {
-    const dim3 grid(a.m_blocks * a.n_blocks * a.splits), block(256);
+    const uint32_t units = a.m_blocks * a.n_blocks * a.splits, room = tile == 256 ? kCus : 2u * kCus;
+    const dim3 grid(units < room ? units : room), block(256);
     if (tile == 256) hipLaunchKernelGGL((linear_kernel<DT, AL, BL, EPI, 256>), grid, block, 0, s, a);
     else hipLaunchKernelGGL((linear_kernel<DT, AL, BL, EPI, 128>), grid, block, 0, s, a);
 }
@@ -38,7 +40,9 @@ void LinearOf<DT>::sum(const LinSumArgs& a, hipStream_t s) {
 template <>
 void LinearOf<DT>::gated_slope(const GatedGradArgs& a, hipStream_t s) {
     const uint64_t groups = (uint64_t)a.rows * ((a.filled / 8u + 255u) / 256u);
-    hipLaunchKernelGGL(gated_slope_kernel<DT>, dim3((unsigned)(groups < 4096u ? groups : 4096u)), dim3(256), 0, s, a);
+    const dim3 grid((unsigned)(groups < 4096u ? groups : 4096u)), block(256);
+    if (a.act == kActBell) hipLaunchKernelGGL((gated_slope_kernel<DT, true>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((gated_slope_kernel<DT, false>), grid, block, 0, s, a);
 }
 
 template <>
