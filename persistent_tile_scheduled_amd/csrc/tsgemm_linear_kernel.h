@@ -154,10 +154,13 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
     }
 }
 
-// 8 consecutive values of a row as 16-bit ones, as far as `count` of them exist.
+// 8 consecutive values of a row as 16-bit ones: all of them, or as far as `count` of
+// them exist.
 template <int DT>
-__device__ __forceinline__ void store8(uint16_t* to, const float* v, uint32_t count) {
-    const u32x4 w = {pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3]), pack2<DT>(v[4], v[5]), pack2<DT>(v[6], v[7])};
+__device__ __forceinline__ u32x4 pack8(const float* v) {
+    return u32x4{pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3]), pack2<DT>(v[4], v[5]), pack2<DT>(v[6], v[7])};
+}
+__device__ __forceinline__ void store_some(uint16_t* to, u32x4 w, uint32_t count) {
     if (count >= 8u) {
         *(u32x4_at2*)to = w;
     } else {
@@ -165,6 +168,20 @@ __device__ __forceinline__ void store8(uint16_t* to, const float* v, uint32_t co
         for (uint32_t e = 0; e < 7u; ++e)
             if (e < count) to[e] = (uint16_t)(w[e / 2] >> (16 * (e % 2)));
     }
+}
+template <int DT>
+__device__ __forceinline__ void store8(uint16_t* to, const float* v, uint32_t count) {
+    store_some(to, pack8<DT>(v), count);
+}
+
+// The largest value and the sum over the four lanes that hold a row's columns.
+__device__ __forceinline__ float max_over_groups(float x) {
+    const float y = fmaxf(x, __shfl_xor(x, 16));
+    return fmaxf(y, __shfl_xor(y, 32));
+}
+__device__ __forceinline__ float sum_over_groups(float x) {
+    const float y = x + __shfl_xor(x, 16);
+    return y + __shfl_xor(y, 32);
 }
 
 // Tile and range of slabs of one unit of work.
@@ -479,6 +496,17 @@ __global__ __launch_bounds__(256, T == 256 ? 1 : 2) void linear_kernel(LinArgs a
     for (uint32_t unit = first_unit; unit < units; unit += workers) {
     const LinUnit u = lin_unit(args, unit);
     const uint32_t m0 = u.m_idx * T, n0 = u.n_idx * (EPI == LIN_GATED ? WT : T);  // a gated tile holds T/2 columns of each projection
+    // what the epilogue needs of the tile's rows is on its way while the products are formed
+    int64_t row_target[EPI == LIN_LSE ? F : 1];
+    LossRow row_info[EPI == LIN_DLOGITS ? F : 1];
+    if constexpr (EPI == LIN_LSE || EPI == LIN_DLOGITS) {
+#pragma unroll
+        for (int fm = 0; fm < F; ++fm) {
+            const uint32_t m = m0 + wr * WT + 16u * fm + l16, at = m < args.M ? m : args.M - 1u;
+            if constexpr (EPI == LIN_LSE) row_target[fm] = args.target[at];
+            else row_info[fm] = args.row[at];
+        }
+    }
     phase(FALSE_{}, TRUE_{});
     phase(TRUE_{}, TRUE_{});
     for (uint32_t s = 1; s < u.slabs; ++s) {
@@ -513,109 +541,192 @@ __global__ __launch_bounds__(256, T == 256 ? 1 : 2) void linear_kernel(LinArgs a
     };
     auto left = [](uint32_t at, uint32_t end) __attribute__((always_inline)) -> uint32_t { return at < end ? end - at : 0u; };
 
+    // Every epilogue comes in two copies: for a tile that lies inside the matrix, with
+    // nothing to ask, and for one that does not.
+    const bool inside = m0 + T <= args.M && n0 + (EPI == LIN_GATED ? WT : T) <= args.N;
+
     if constexpr (EPI == LIN_GATED) {
         const Act act(args.act);
-        auto gated = [&](auto bell_c) __attribute__((always_inline)) {
+        auto gated = [&](auto bell_c, auto inside_c) __attribute__((always_inline)) {
+            constexpr bool BELL = decltype(bell_c)::value, INSIDE = decltype(inside_c)::value;
 #pragma unroll
             for (int fm = 0; fm < F; ++fm) {
-                const uint32_t m = row_of(fm);
+                const uint32_t m = row_of(fm), n = n0 + wc * (WT / 2) + 8u * lg;
+                uint16_t* const y_at = args.y + (int64_t)m * args.ldy + n;
+                uint16_t* const gate_at = args.gate + (int64_t)m * args.ldgate + n;
+                uint16_t* const up_at = args.up + (int64_t)m * args.ldup + n;
 #pragma unroll
                 for (int t = 0; t < F / 4; ++t) {
                     float g[8], up[8], y[8], bell;
                     eight(fm, t, g);
                     eight(fm, t + F / 4, up);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) y[e] = g[e] * act_share<decltype(bell_c)::value>(act, g[e], bell) * up[e];
-                    const uint32_t n = n0 + wc * (WT / 2) + 32u * t + 8u * lg;
-                    const uint32_t count = m < args.M ? left(n, args.N) : 0u;
-                    if (count != 0u) {
-                        store8<DT>(args.y + (int64_t)m * args.ldy + n, y, count);
-                        if (args.gate) store8<DT>(args.gate + (int64_t)m * args.ldgate + n, g, count);
-                        if (args.up) store8<DT>(args.up + (int64_t)m * args.ldup + n, up, count);
+                    for (int e = 0; e < 8; ++e) y[e] = g[e] * act_share<BELL>(act, g[e], bell) * up[e];
+                    const uint32_t count = INSIDE ? 8u : m < args.M ? left(n + 32u * t, args.N) : 0u;
+                    if (INSIDE || count != 0u) {
+                        store8<DT>(y_at + 32 * t, y, count);
+                        if (args.gate) store8<DT>(gate_at + 32 * t, g, count);
+                        if (args.up) store8<DT>(up_at + 32 * t, up, count);
                     }
                 }
             }
         };
-        if (args.act == kActBell) gated(TRUE_{});
-        else gated(FALSE_{});
+        if (args.act == kActBell) inside ? gated(TRUE_{}, TRUE_{}) : gated(TRUE_{}, FALSE_{});
+        else inside ? gated(FALSE_{}, TRUE_{}) : gated(FALSE_{}, FALSE_{});
     } else if constexpr (EPI == LIN_LSE) {
+        // Every lane's sum is of powers of 2 relative to its own largest logit; the four
+        // lanes of a row meet afterwards, all rows at once.
+        float top[F], sum[F];
+        const uint32_t c0 = n0 + wc * WT;
+        auto sums = [&](auto inside_c) __attribute__((always_inline)) {
+            constexpr bool INSIDE = decltype(inside_c)::value;
+            const uint32_t n = c0 + 8u * lg;
+#pragma unroll
+            for (int fm = 0; fm < F; ++fm) {
+                float v[F / 2][8];
+#pragma unroll
+                for (int t = 0; t < F / 2; ++t) {
+                    eight(fm, t, v[t]);
+                    if constexpr (!INSIDE) {
+#pragma unroll
+                        for (uint32_t e = 0; e < 8; ++e)
+                            if (n + 32u * t + e >= args.N) v[t][e] = -__builtin_inff();
+                    }
+                }
+                float a = -__builtin_inff(), b = a;
+#pragma unroll
+                for (int t = 0; t < F / 2; ++t)
+#pragma unroll
+                    for (int e = 0; e < 8; e += 4) {
+                        a = fmaxf(fmaxf(a, v[t][e]), v[t][e + 1]);
+                        b = fmaxf(fmaxf(b, v[t][e + 2]), v[t][e + 3]);
+                    }
+                a = fmaxf(a, b);
+                top[fm] = a == -__builtin_inff() ? a : a * kLog2e;
+                const float from = a == -__builtin_inff() ? 0.0f : a * kLog2e;  // the sum is in units of 2^from
+                float s0 = 0.0f, s1 = 0.0f;
+#pragma unroll
+                for (int t = 0; t < F / 2; ++t)
+#pragma unroll
+                    for (int e = 0; e < 8; e += 2) {
+                        s0 += __builtin_amdgcn_exp2f(__builtin_fmaf(v[t][e], kLog2e, -from));
+                        s1 += __builtin_amdgcn_exp2f(__builtin_fmaf(v[t][e + 1], kLog2e, -from));
+                    }
+                sum[fm] = s0 + s1;
+                __builtin_amdgcn_sched_barrier(0);  // one row of blocks after the other: they do not fit the registers
+            }
+        };
+        if (inside) sums(TRUE_{});
+        else sums(FALSE_{});
+        // the targets' logits, where they are among the wave's columns: seldom
 #pragma unroll
         for (int fm = 0; fm < F; ++fm) {
-            const uint32_t m = row_of(fm);
-            const int64_t target = m < args.M ? args.target[m] : -1;
-            float v[F / 2][8], top = -__builtin_inff();
+            const uint32_t at = (uint32_t)row_target[fm] - c0, m = row_of(fm);
+            const bool here = row_target[fm] >= (int64_t)c0 && row_target[fm] < (int64_t)c0 + WT && row_target[fm] < (int64_t)args.N &&
+                              (at / 8u) % 4u == lg && m < args.M;
+            if (__builtin_amdgcn_ballot_w64(here) == 0u) continue;
+            float hit = 0.0f;
 #pragma unroll
-            for (int t = 0; t < F / 2; ++t) {
-                eight(fm, t, v[t]);
-                const uint32_t n = n0 + wc * WT + 32u * t + 8u * lg;
+            for (uint32_t t = 0; t < F / 2; ++t) {
+                float v[8];
+                eight(fm, t, v);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    if (n + e >= args.N) v[t][e] = -__builtin_inff();
-                    else if (target == (int64_t)(n + e)) args.hit[m] = v[t][e];
-                    top = fmaxf(top, v[t][e]);
-                }
+                for (uint32_t e = 0; e < 8; ++e) hit = at == 32u * t + 8u * lg + e ? v[e] : hit;
             }
-            top = fmaxf(top, __shfl_xor(top, 16));
-            top = fmaxf(top, __shfl_xor(top, 32));
-            const float from = top == -__builtin_inff() ? 0.0f : top * kLog2e;  // the sum is in units of 2^from
-            float sum = 0.0f;
+            if (here) args.hit[m] = hit;
+        }
 #pragma unroll
-            for (int t = 0; t < F / 2; ++t)
-#pragma unroll
-                for (int e = 0; e < 8; ++e) sum += __builtin_amdgcn_exp2f(__builtin_fmaf(v[t][e], kLog2e, -from));
-            sum += __shfl_xor(sum, 16);
-            sum += __shfl_xor(sum, 32);
-            if (lg == 0u && m < args.M) args.part[(size_t)(u.n_idx * 2u + wc) * args.M + m] = make_float2(top == -__builtin_inff() ? top : from, sum);
+        for (int fm = 0; fm < F; ++fm) {
+            const float all = max_over_groups(top[fm]);
+            const float s = sum_over_groups(sum[fm] * __builtin_amdgcn_exp2f(top[fm] - (all == -__builtin_inff() ? 0.0f : all)));
+            const uint32_t m = row_of(fm);
+            if (lg == 0u && m < args.M) args.part[(size_t)(u.n_idx * 2u + wc) * args.M + m] = make_float2(all, s);
         }
     } else if constexpr (EPI == LIN_DLOGITS) {
+        const uint32_t c0 = n0 + wc * WT;
+        auto gradient = [&](auto inside_c) __attribute__((always_inline)) {
+            constexpr bool INSIDE = decltype(inside_c)::value;
+            const uint32_t n = c0 + 8u * lg;
 #pragma unroll
-        for (int fm = 0; fm < F; ++fm) {
-            const uint32_t m = row_of(fm);
-            if (m >= args.M) continue;
-            const LossRow r = args.row[m];
+            for (int fm = 0; fm < F; ++fm) {
+                const uint32_t m = row_of(fm);
+                const LossRow r = row_info[fm];
+                const uint32_t at = (uint32_t)r.target - args.first - c0;  // of the wave's columns, if below WT
+                const bool some = __builtin_amdgcn_ballot_w64(r.target >= 0 && at < (uint32_t)WT) != 0u;
+                uint16_t* const to = args.dl + (int64_t)m * args.lddl + n;
 #pragma unroll
-            for (int t = 0; t < F / 2; ++t) {
-                float v[8];
-                eight(fm, t, v);
-                const uint32_t n = n0 + wc * WT + 32u * t + 8u * lg;
+                for (int t = 0; t < F / 2; ++t) {
+                    float v[8];
+                    eight(fm, t, v);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(v[e], kLog2e, -r.lse2));
-                    const bool is = r.target == (int32_t)(args.first + n + e);
-                    v[e] = r.target < 0 || n + e >= args.N ? 0.0f : r.d * (is ? p - 1.0f : p);
-                }
-                store8<DT>(args.dl + (int64_t)m * args.lddl + n, v, 8u);
-            }
-        }
-    } else {
-        const float scale = args.unscale ? *args.unscale : 1.0f;
+                    for (int e = 0; e < 8; ++e) v[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(v[e], kLog2e, -r.lse2));
+                    if (some) {
 #pragma unroll
-        for (int fm = 0; fm < F; ++fm) {
-            const uint32_t m = row_of(fm);
-            const bool upper = m >= args.half;
-            const uint32_t mo = upper ? m - args.half : m;
-            if (m >= args.M || mo >= args.out_rows) continue;
-#pragma unroll
-            for (int t = 0; t < F / 2; ++t) {
-                float v[8];
-                eight(fm, t, v);
-                const uint32_t n = n0 + wc * WT + 32u * t + 8u * lg;
-                if (n >= args.N) continue;  // N is a multiple of 8
-                if (args.sums) {
-                    float* to = args.sums + ((size_t)u.split * args.M + m) * args.N + n;
-                    f32x4 x = {v[0], v[1], v[2], v[3]}, y = {v[4], v[5], v[6], v[7]};
-                    if (args.add) {
-                        x += *(const f32x4*)to;
-                        y += *(const f32x4*)(to + 4);
+                        for (uint32_t e = 0; e < 8; ++e) v[e] -= at == 32u * t + 8u * lg + e ? 1.0f : 0.0f;
                     }
-                    *(f32x4*)to = x;
-                    *(f32x4*)(to + 4) = y;
-                } else {
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) v[e] *= scale;
-                    store8<DT>((upper ? args.out2 + (int64_t)mo * args.ldo2 : args.out + (int64_t)mo * args.ldo) + n, v, 8u);
+                    for (uint32_t e = 0; e < 8; ++e) {
+                        v[e] *= r.d;
+                        if constexpr (!INSIDE) v[e] = n + 32u * t + e >= args.N ? 0.0f : v[e];
+                    }
+                    u32x4 w = pack8<DT>(v);
+                    if (r.target < 0) w = u32x4{0u, 0u, 0u, 0u};  // whatever its logits are
+                    if (INSIDE || m < args.M) *(u32x4*)(to + 32 * t) = w;
                 }
             }
+        };
+        if (inside) gradient(TRUE_{});
+        else gradient(FALSE_{});
+    } else {
+        // whole tiles belong to one half: `half` is a multiple of T or past the end
+        const bool upper = m0 >= args.half;
+        const uint32_t rows = upper ? args.half + args.out_rows : args.out_rows, end = rows < args.M ? rows : args.M;
+        const bool whole = m0 + T <= end && n0 + T <= args.N;
+        if (args.sums) {
+            auto add_up = [&](auto whole_c, auto add_c) __attribute__((always_inline)) {
+#pragma unroll
+                for (int fm = 0; fm < F; ++fm) {
+                    const uint32_t m = row_of(fm), n = n0 + wc * WT + 8u * lg;
+                    float* const at = args.sums + ((size_t)u.split * args.M + m) * args.N + n;
+#pragma unroll
+                    for (int t = 0; t < F / 2; ++t) {
+                        float v[8];
+                        eight(fm, t, v);
+                        if (!decltype(whole_c)::value && (m >= end || n + 32u * t >= args.N)) continue;  // N is a multiple of 8
+                        f32x4 x = {v[0], v[1], v[2], v[3]}, y = {v[4], v[5], v[6], v[7]};
+                        if constexpr (decltype(add_c)::value) {
+                            x += *(const f32x4*)(at + 32 * t);
+                            y += *(const f32x4*)(at + 32 * t + 4);
+                        }
+                        *(f32x4*)(at + 32 * t) = x;
+                        *(f32x4*)(at + 32 * t + 4) = y;
+                    }
+                }
+            };
+            if (whole) args.add ? add_up(TRUE_{}, TRUE_{}) : add_up(TRUE_{}, FALSE_{});
+            else args.add ? add_up(FALSE_{}, TRUE_{}) : add_up(FALSE_{}, FALSE_{});
+        } else {
+            const float scale = args.unscale ? *args.unscale : 1.0f;
+            uint16_t* const out = upper ? args.out2 - (int64_t)args.half * args.ldo2 : args.out;
+            const int64_t ld = upper ? args.ldo2 : args.ldo;
+            auto round_off = [&](auto whole_c) __attribute__((always_inline)) {
+#pragma unroll
+                for (int fm = 0; fm < F; ++fm) {
+                    const uint32_t m = row_of(fm), n = n0 + wc * WT + 8u * lg;
+                    uint16_t* const at = out + (int64_t)m * ld + n;
+#pragma unroll
+                    for (int t = 0; t < F / 2; ++t) {
+                        float v[8];
+                        eight(fm, t, v);
+                        if (!decltype(whole_c)::value && (m >= end || n + 32u * t >= args.N)) continue;
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) v[e] *= scale;
+                        *(u32x4*)(at + 32 * t) = pack8<DT>(v);
+                    }
+                }
+            };
+            if (whole) round_off(TRUE_{});
+            else round_off(FALSE_{});
         }
     }
     }

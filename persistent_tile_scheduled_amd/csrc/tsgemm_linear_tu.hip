@@ -51,19 +51,27 @@ void LinearOf<DT>::loss_rows(const LossGradArgs& a, hipStream_t s) {
 }
 
 #if TSG_LIN_DT == 1  // what no type goes by
-// 16 rows a workgroup, 16 threads a row: sum of 2^e s over the parts, each
-// thread's over every 16th part in order, then over the threads in order.
-__global__ __launch_bounds__(256) void loss_join_kernel(LossArgs a) {
-    __shared__ float tops[16][16], sums[16][16];
+// 16 rows a workgroup, 64 threads a row: sum of 2^e s over the parts, each thread's
+// over every 64th part, eight requested at a time, then over the threads in order.
+__global__ __launch_bounds__(1024) void loss_join_kernel(LossArgs a) {
+    __shared__ float tops[64][16], sums[64][16];
     const uint32_t i = threadIdx.x & 15u, j = threadIdx.x >> 4;
     const int64_t r = (int64_t)blockIdx.x * 16 + i;
     const auto zero_if_none = [](float e) { return e == -__builtin_inff() ? 0.0f : e; };
     float top = -__builtin_inff(), sum = 0.0f;
     if (r < a.rows) {
-        for (uint32_t p = j; p < a.parts; p += 16u) {
-            const float2 v = a.part[(size_t)p * a.rows + r];
-            const float t = fmaxf(top, v.x), from = zero_if_none(t);
-            sum = sum * __builtin_amdgcn_exp2f(top - from) + v.y * __builtin_amdgcn_exp2f(v.x - from);
+        for (uint32_t p = j; p < a.parts; p += 512u) {
+            float2 v[8];
+            float t = top;
+#pragma unroll
+            for (uint32_t k = 0; k < 8; ++k)
+                v[k] = p + 64u * k < a.parts ? a.part[(size_t)(p + 64u * k) * a.rows + r] : make_float2(-__builtin_inff(), 0.0f);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) t = fmaxf(t, v[k].x);
+            const float from = zero_if_none(t);
+            sum *= __builtin_amdgcn_exp2f(top - from);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) sum += v[k].y * __builtin_amdgcn_exp2f(v[k].x - from);
             top = t;
         }
     }
@@ -71,10 +79,10 @@ __global__ __launch_bounds__(256) void loss_join_kernel(LossArgs a) {
     sums[j][i] = sum;
     __syncthreads();
     if (j != 0u || r >= a.rows) return;
-    for (int k = 1; k < 16; ++k) top = fmaxf(top, tops[k][i]);
+    for (int k = 1; k < 64; ++k) top = fmaxf(top, tops[k][i]);
     const float from = zero_if_none(top);
     sum = 0.0f;
-    for (int k = 0; k < 16; ++k) sum += sums[k][i] * __builtin_amdgcn_exp2f(tops[k][i] - from);
+    for (int k = 0; k < 64; ++k) sum += sums[k][i] * __builtin_amdgcn_exp2f(tops[k][i] - from);
     // in fp64, divided by what the logits were multiplied with: the loss is the
     // difference of two numbers that may be close
     const double lse = (double)from / (double)kLog2e + log((double)sum);
@@ -90,7 +98,7 @@ __global__ __launch_bounds__(256) void linear_zero_kernel(uint16_t* out, int64_t
 }
 
 void launch_loss_join(const LossArgs& a, hipStream_t s) {
-    hipLaunchKernelGGL(loss_join_kernel, dim3((unsigned)((a.rows + 15) / 16)), dim3(256), 0, s, a);
+    hipLaunchKernelGGL(loss_join_kernel, dim3((unsigned)((a.rows + 15) / 16)), dim3(1024), 0, s, a);
 }
 
 void launch_linear_zero(uint16_t* out, int64_t ld, int64_t rows, uint32_t width, hipStream_t s) {
