@@ -73,30 +73,31 @@ int64_t aligned(int64_t bytes) { return round_up(bytes, 256); }
 // The gated gradient's products and where they lie in the workspace.
 struct GatedGradPlan {
     LinShape dx, dw;
-    int64_t pitch, d, sums, bytes;  // sums: of either product, one after the other
+    int64_t pitch, ld, sums, bytes;  // sums: of either product, one after the other
     GatedGradPlan(int64_t rows, int64_t hidden, int64_t width) {
         pitch = gated_pitch(hidden);
         dx = linear_shape(rows, width, 2 * slabs_of(hidden), false, true);
         dw = linear_shape(2 * pitch, width, slabs_of(rows), false, true);
         const int64_t x = dx.splits > 1 ? dx.splits * rows * width * 4 : 0, w = dw.splits > 1 ? dw.splits * 2 * pitch * width * 4 : 0;
-        d = 0;
-        sums = aligned(rows * 2 * pitch * 2);
+        ld = 2 * pitch;
+        sums = aligned(rows * ld * 2);
         bytes = sums + aligned(x > w ? x : w);
     }
 };
 
 struct LossPlan {
     LinShape s;
-    int64_t hit, bytes;
+    int64_t parts, hit, bytes;
     LossPlan(int64_t rows, int64_t vocab, int64_t width) {
         s = linear_shape(rows, vocab, slabs_of(width), false, false);
-        hit = aligned(2 * s.n_blocks * rows * 8);
+        parts = rows <= kFewRows ? few_groups(vocab) : 2 * s.n_blocks;
+        hit = aligned(parts * rows * 8);
         bytes = hit + aligned(rows * 4);
     }
 };
 
 struct LossGradPlan {
-    int64_t piece, unscale, x, dl, dx_sums, dw_sums, bytes;
+    int64_t piece, ld, ldx, unscale, x, dl, dx_sums, dw_sums, bytes;
     LinShape logits, dx, dw;  // of a whole piece
     LossGradPlan(int64_t rows, int64_t vocab, int64_t width) {
         piece = vocab_piece(rows, vocab);
@@ -104,9 +105,11 @@ struct LossGradPlan {
         dx = linear_shape(rows, width, piece / 64, false, true);
         dw = linear_shape(piece, width, slabs_of(rows), false, true);
         unscale = aligned(rows * 16);
+        ld = piece;
+        ldx = width;
         x = unscale + 256;
-        dl = x + aligned(rows * width * 2);
-        dx_sums = dl + aligned(rows * piece * 2);
+        dl = x + aligned(rows * ldx * 2);
+        dx_sums = dl + aligned(rows * ld * 2);
         dw_sums = dx_sums + (dx.splits > 1 || vocab > piece ? aligned(dx.splits * rows * width * 4) : 0);
         bytes = dw_sums + (dw.splits > 1 ? aligned(dw.splits * piece * width * 4) : 0);
     }
@@ -156,7 +159,10 @@ int tsgemm_gated_linear(int64_t rows, int64_t hidden, int64_t width, int dtype, 
     a.y = static_cast<uint16_t*>(y); a.gate = static_cast<uint16_t*>(gate); a.up = static_cast<uint16_t*>(up);
     a.ldy = ldy; a.ldgate = ldgate; a.ldup = ldup; a.act = act;
     (void)hipGetLastError();
-    of_type(dtype, [&](auto k) { k.product(LIN_KIND_GATED, s.tile, a, static_cast<hipStream_t>(stream)); });
+    of_type(dtype, [&](auto k) {
+        if (rows <= kFewRows) k.few(LIN_KIND_GATED, a, static_cast<hipStream_t>(stream));
+        else k.product(LIN_KIND_GATED, s.tile, a, static_cast<hipStream_t>(stream));
+    });
     return launched("gated linear");
 }
 
@@ -231,13 +237,13 @@ int tsgemm_gated_linear_grad(int64_t rows, int64_t hidden, int64_t width, int dt
     GatedGradArgs g = {};
     g.dy = static_cast<const uint16_t*>(dy); g.gate = static_cast<const uint16_t*>(gate); g.up = static_cast<const uint16_t*>(up);
     g.d = d; g.lddy = lddy; g.ldgate = ldgate; g.ldup = ldup; g.rows = rows; g.act = act;
-    g.hidden = (uint32_t)hidden; g.filled = (uint32_t)round_up(hidden, 64); g.pitch = (uint32_t)plan.pitch;
+    g.hidden = (uint32_t)hidden; g.filled = (uint32_t)round_up(hidden, 64); g.pitch = (uint32_t)plan.pitch; g.ld = plan.ld;
     of_type(dtype, [&](auto k) { k.gated_slope(g, s); });
     rc = launched("gated linear gradient");
     if (rc != TSGEMM_OK) return rc;
     if (dx) {
         LinArgs a = product(plan.dx, rows, width);
-        a.a = d; a.a2 = d + plan.pitch; a.lda = 2 * plan.pitch; a.Ka = g.filled;
+        a.a = d; a.a2 = d + plan.pitch; a.lda = plan.ld; a.Ka = g.filled;
         a.b = static_cast<const uint16_t*>(gate_weight); a.ldb = ldgw;
         a.b2 = static_cast<const uint16_t*>(up_weight); a.ldb2 = lduw; a.Kb = (uint32_t)hidden;
         a.seg_slabs = (uint32_t)slabs_of(hidden);
@@ -252,7 +258,7 @@ int tsgemm_gated_linear_grad(int64_t rows, int64_t hidden, int64_t width, int dt
     }
     if (out_dg) {
         LinArgs a = product(plan.dw, 2 * plan.pitch, width);
-        a.a = d; a.lda = 2 * plan.pitch; a.Ka = a.Kb = (uint32_t)rows;
+        a.a = d; a.lda = plan.ld; a.Ka = a.Kb = (uint32_t)rows;
         a.b = static_cast<const uint16_t*>(x); a.ldb = ldx;
         a.out = out_dg; a.ldo = lddgw; a.out2 = out_du; a.ldo2 = ldduw;
         a.half = (uint32_t)plan.pitch; a.out_rows = (uint32_t)hidden;
@@ -305,12 +311,15 @@ int tsgemm_linear_cross_entropy(int64_t rows, int64_t vocab, int64_t width, int 
     a.part = static_cast<float2*>(workspace);
     a.hit = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + plan.hit);
     (void)hipGetLastError();
-    of_type(dtype, [&](auto k) { k.product(LIN_KIND_LSE, plan.s.tile, a, s); });
+    of_type(dtype, [&](auto k) {
+        if (rows <= kFewRows) k.few(LIN_KIND_LSE, a, s);
+        else k.product(LIN_KIND_LSE, plan.s.tile, a, s);
+    });
     rc = launched("linear cross entropy");
     if (rc != TSGEMM_OK) return rc;
     LossArgs j = {};
     j.part = a.part; j.hit = a.hit; j.target = target; j.loss = loss; j.lse = lse; j.ignore = ignore_index;
-    j.rows = rows; j.parts = 2 * a.n_blocks; j.vocab = (uint32_t)vocab;
+    j.rows = rows; j.parts = (uint32_t)plan.parts; j.vocab = (uint32_t)vocab;
     launch_loss_join(j, s);
     return launched("linear cross entropy join");
 }
@@ -367,7 +376,7 @@ int tsgemm_linear_cross_entropy_grad(int64_t rows, int64_t vocab, int64_t width,
     g.dloss = dloss; g.lse = lse; g.target = target; g.x = static_cast<const uint16_t*>(x); g.ldx = ldx;
     g.counted_x = dweight ? reinterpret_cast<uint16_t*>(w + plan.x) : nullptr;
     g.row = reinterpret_cast<LossRow*>(w); g.unscale = reinterpret_cast<float*>(w + plan.unscale);
-    g.ignore = ignore_index; g.rows = rows; g.width = (uint32_t)width; g.vocab = (uint32_t)vocab;
+    g.ldcx = plan.ldx; g.ignore = ignore_index; g.rows = rows; g.width = (uint32_t)width; g.vocab = (uint32_t)vocab;
     (void)hipGetLastError();
     of_type(dtype, [&](auto k) { k.loss_rows(g, s); });
     rc = launched("linear cross entropy gradient");
@@ -377,12 +386,12 @@ int tsgemm_linear_cross_entropy_grad(int64_t rows, int64_t vocab, int64_t width,
         const uint16_t* const wp = static_cast<const uint16_t*>(weight) + first * ldw;
         LinArgs l = product(plan.logits, rows, columns);
         l.a = g.x; l.lda = ldx; l.b = wp; l.ldb = ldw; l.Ka = l.Kb = (uint32_t)width;
-        l.row = g.row; l.dl = dl; l.lddl = plan.piece; l.first = (uint32_t)first;
+        l.row = g.row; l.dl = dl; l.lddl = plan.ld; l.first = (uint32_t)first;
         of_type(dtype, [&](auto k) { k.product(LIN_KIND_DLOGITS, plan.logits.tile, l, s); });
         rc = launched("linear cross entropy gradient of the logits");
         if (rc == TSGEMM_OK && dx) {
             LinArgs a = product(plan.dx, rows, width);
-            a.a = dl; a.lda = plan.piece; a.Ka = (uint32_t)plan.piece;
+            a.a = dl; a.lda = plan.ld; a.Ka = (uint32_t)plan.piece;
             a.b = wp; a.ldb = ldw; a.Kb = (uint32_t)columns;
             a.out = out_dx; a.ldo = lddx; a.out_rows = (uint32_t)rows; a.unscale = g.unscale;
             if (plan.dx.splits > 1 || several) a.sums = reinterpret_cast<float*>(w + plan.dx_sums);
@@ -395,7 +404,7 @@ int tsgemm_linear_cross_entropy_grad(int64_t rows, int64_t vocab, int64_t width,
         }
         if (rc == TSGEMM_OK && dweight) {
             LinArgs a = product(plan.dw, plan.piece, width);
-            a.a = dl; a.lda = plan.piece; a.b = g.counted_x; a.ldb = width; a.Ka = a.Kb = (uint32_t)rows;
+            a.a = dl; a.lda = plan.ld; a.b = g.counted_x; a.ldb = plan.ldx; a.Ka = a.Kb = (uint32_t)rows;
             a.out = out_dw + first * lddw; a.ldo = lddw; a.out_rows = (uint32_t)columns; a.unscale = g.unscale;
             if (plan.dw.splits > 1) a.sums = reinterpret_cast<float*>(w + plan.dw_sums);
             of_type(dtype, [&](auto k) {

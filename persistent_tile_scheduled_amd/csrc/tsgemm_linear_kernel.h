@@ -160,9 +160,12 @@ template <int DT>
 __device__ __forceinline__ u32x4 pack8(const float* v) {
     return u32x4{pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3]), pack2<DT>(v[4], v[5]), pack2<DT>(v[6], v[7])};
 }
+// Whole chunks go past the caches (nt): y, gate and up, which nothing reads soon, would
+// evict slabs that the XCD's other workgroups are still to read (all three kept at 8192 x
+// 4096 x 8192 bf16: 2500 -> 2210 cycles a slab).
 __device__ __forceinline__ void store_some(uint16_t* to, u32x4 w, uint32_t count) {
     if (count >= 8u) {
-        *(u32x4_at2*)to = w;
+        __builtin_nontemporal_store((u32x4_at2)w, (u32x4_at2*)to);
     } else {
 #pragma unroll
         for (uint32_t e = 0; e < 7u; ++e)
@@ -370,26 +373,22 @@ __global__ __launch_bounds__(256, T == 256 ? 1 : 2) void linear_kernel(LinArgs a
 #pragma unroll
     for (int i = 0; i < AB; ++i) b_off[i] = lds_base + STAGE + offset(B_ALONG, wc, i);
     i16x4 fa[F][2][2], fb[F][2][2];  // [block][k-step][half]
-    auto read = [&](auto along_c, i16x4 (&to)[2], const uint32_t* at, auto f_c, auto k_c) __attribute__((always_inline)) {
-        constexpr int f = decltype(f_c)::value, k = decltype(k_c)::value;
-        if constexpr (decltype(along_c)::value) {
+    // LDS read i of those of half a side's blocks, both k-steps: 16 bytes a lane along
+    // the sum, 8 across it
+    constexpr int RA = A_ALONG ? F : 2 * F, RB = B_ALONG ? F : 2 * F;
+    auto read = [&](auto along_c, i16x4 (&to)[F][2][2], const uint32_t* at, auto half_c, auto i_c) __attribute__((always_inline)) {
+        constexpr bool ALONG = decltype(along_c)::value;
+        constexpr int i = decltype(i_c)::value, f = decltype(half_c)::value * F / 2 + (ALONG ? i / 2 : i / 4), k = (ALONG ? i : i / 2) % 2;
+        if constexpr (ALONG) {
             const i16x8 v = __builtin_bit_cast(i16x8, *(const lds_u32x4*)((lds_u8*)(uintptr_t)at[k] + f * 2048));
-            to[0] = __builtin_shufflevector(v, v, 0, 1, 2, 3);
-            to[1] = __builtin_shufflevector(v, v, 4, 5, 6, 7);
+            to[f][k][0] = __builtin_shufflevector(v, v, 0, 1, 2, 3);
+            to[f][k][1] = __builtin_shufflevector(v, v, 4, 5, 6, 7);
         } else {
-            to[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)((lds_u8*)(uintptr_t)at[f] + k * 32 * (T * 2)));
-            to[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)((lds_u8*)(uintptr_t)at[f] + (k * 32 + 4) * (T * 2)));
+            to[f][k][i % 2] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)((lds_u8*)(uintptr_t)at[f] + (k * 32 + i % 2 * 4) * (T * 2)));
         }
     };
-    // read i of F of half a side's blocks, both k-steps
-    auto read_a = [&](auto half_c, auto i_c) __attribute__((always_inline)) {
-        constexpr int f = decltype(half_c)::value * F / 2 + decltype(i_c)::value / 2, k = decltype(i_c)::value % 2;
-        read(std::integral_constant<bool, A_ALONG>{}, fa[f][k], a_at, std::integral_constant<int, f>{}, std::integral_constant<int, k>{});
-    };
-    auto read_b = [&](auto half_c, auto i_c) __attribute__((always_inline)) {
-        constexpr int f = decltype(half_c)::value * F / 2 + decltype(i_c)::value / 2, k = decltype(i_c)::value % 2;
-        read(std::integral_constant<bool, B_ALONG>{}, fb[f][k], b_at, std::integral_constant<int, f>{}, std::integral_constant<int, k>{});
-    };
+    auto read_a = [&](auto half_c, auto i_c) __attribute__((always_inline)) { read(std::integral_constant<bool, A_ALONG>{}, fa, a_at, half_c, i_c); };
+    auto read_b = [&](auto half_c, auto i_c) __attribute__((always_inline)) { read(std::integral_constant<bool, B_ALONG>{}, fb, b_at, half_c, i_c); };
     auto address = [&](auto i_c, uint32_t stage) __attribute__((always_inline)) {
         constexpr int i = decltype(i_c)::value;
         if constexpr (i < AB) b_at[i] = b_off[i] + stage;
@@ -418,16 +417,29 @@ __global__ __launch_bounds__(256, T == 256 ? 1 : 2) void linear_kernel(LinArgs a
     constexpr int LATE = DF < NL ? START + (NL - 1 - DF) * SPACE + 1 : 0;     // phase 1: gap after its DMAs
     constexpr int STEP_AT = DF < NL ? LATE : START + (DF - 1) * SPACE + 1;    // the loader's step, in phase 1 or 2
     static_assert(STEP_AT + PIECES <= STEPS, "the loader's step needs gaps");
-    constexpr auto refill = [](int i) constexpr {  // phase 2: gap of read i of A's first half
-        int gap = START + F;
-        for (int j = 0; j <= i; ++j) {
-            const int free = (j / 2) * F + F - 1 + kGap;
-            gap = gap > free ? gap : free;
-            if (j < i) ++gap;
+    // The gap of each LDS read of a phase, in order: PER a gap and none before what it
+    // overwrites is used up.  One a gap where there are gaps enough: the four waves' reads
+    // of 8 bytes a lane fill the LDS's time of one MFMA.
+    constexpr int PER = T == 256 ? 1 : 2, LATER = T == 256 ? 2 : 1;
+    constexpr auto read_gap = [](int phase, int op) constexpr {
+        int gap = START, count = 0;
+        for (int i = 0;; ++i) {
+            int from = START;
+            if (phase == 1 && i >= RA) from = START + (RA + PER - 1) / PER + (i - RA) * LATER / PER;  // the second half of B: for phase 2
+            if (phase == 2 && i >= RB) from = ((i - RB) / (2 * RA / F)) * F + F - 1 + kGap;              // A: a row of blocks once it is used up
+            if (gap < from) {
+                gap = from;
+                count = 0;
+            }
+            if (count == PER) {
+                ++gap;
+                count = 0;
+            }
+            if (i == op) return gap;
+            ++count;
         }
-        return gap;
     };
-    static_assert(refill(F - 1) < STEPS && START + 2 * F <= STEPS, "every read needs a gap");
+    static_assert(read_gap(1, RA + RB - 1) < STEPS && read_gap(2, RA + RB - 1) < STEPS, "every read needs a gap");
     using I0 = std::integral_constant<int, 0>;
     using I1 = std::integral_constant<int, 1>;
     using TRUE_ = std::integral_constant<bool, true>;
@@ -435,7 +447,6 @@ __global__ __launch_bounds__(256, T == 256 ? 1 : 2) void linear_kernel(LinArgs a
     uint32_t stage = 0;  // of the slab at hand: 0 or 2 * STAGE
     auto phase = [&](auto second_c, auto clear_c) __attribute__((always_inline)) {
         constexpr bool SECOND = decltype(second_c)::value, CLEAR = decltype(clear_c)::value;
-        constexpr int B_SPACE = T == 256 ? 2 : 1;
         static_for<0, STEPS>([&](auto s_c) __attribute__((always_inline)) {
             constexpr int s = decltype(s_c)::value, k = s % 2;
             constexpr int fm = s / F, j = (s % F) / 2, fn = (SECOND ? F / 2 : 0) + ((fm & 1) ? F / 2 - 1 - j : j);
@@ -456,15 +467,15 @@ __global__ __launch_bounds__(256, T == 256 ? 1 : 2) void linear_kernel(LinArgs a
                 constexpr int i = s - START;
                 if constexpr (SECOND ? i % SPACE == 0 && i / SPACE < DF : i % SPACE == 0 && i / SPACE < NL - DF)
                     dma_op(std::integral_constant<int, (SECOND ? 0 : DF) + i / SPACE>{});
-                if constexpr (SECOND) {
-                    if constexpr (i < F) read_b(I0{}, std::integral_constant<int, i>{});
-                    static_for<0, F>([&](auto r_c) __attribute__((always_inline)) {
-                        if constexpr (refill(decltype(r_c)::value) == s) read_a(I0{}, r_c);
-                    });
-                } else {
-                    if constexpr (i < F) read_a(I1{}, std::integral_constant<int, i>{});
-                    else if constexpr ((i - F) % B_SPACE == 0 && (i - F) / B_SPACE < F) read_b(I1{}, std::integral_constant<int, (i - F) / B_SPACE>{});
-                }
+                static_for<0, RA + RB>([&](auto r_c) __attribute__((always_inline)) {
+                    constexpr int r = decltype(r_c)::value;
+                    if constexpr (read_gap(SECOND ? 2 : 1, r) == s) {
+                        if constexpr (SECOND && r < RB) read_b(I0{}, r_c);
+                        else if constexpr (SECOND) read_a(I0{}, std::integral_constant<int, r - RB>{});
+                        else if constexpr (r < RA) read_a(I1{}, r_c);
+                        else read_b(I1{}, std::integral_constant<int, r - RA>{});
+                    }
+                });
             }
             if constexpr (SECOND == (DF == NL) && s >= STEP_AT && s < STEP_AT + PIECES) step(std::integral_constant<int, s - STEP_AT>{});
             if constexpr (s + 1 >= START) {
@@ -490,8 +501,8 @@ __global__ __launch_bounds__(256, T == 256 ? 1 : 2) void linear_kernel(LinArgs a
     lds_barrier();
     pause();
     static_for<0, AA + AB>([&](auto i_c) __attribute__((always_inline)) { address(i_c, 0u); });
-    static_for<0, F>([&](auto i_c) __attribute__((always_inline)) { read_b(I0{}, i_c); });
-    static_for<0, F>([&](auto i_c) __attribute__((always_inline)) { read_a(I0{}, i_c); });
+    static_for<0, RB>([&](auto i_c) __attribute__((always_inline)) { read_b(I0{}, i_c); });
+    static_for<0, RA>([&](auto i_c) __attribute__((always_inline)) { read_a(I0{}, i_c); });
 
     for (uint32_t unit = first_unit; unit < units; unit += workers) {
     const LinUnit u = lin_unit(args, unit);

@@ -20,8 +20,8 @@ struct GatedGradArgs {
     const uint16_t* dy;
     const uint16_t* gate;
     const uint16_t* up;
-    uint16_t* d;     // [rows][2 pitch]: dg, then du from column `pitch` on
-    int64_t lddy, ldgate, ldup;
+    uint16_t* d;     // [rows][ld]: dg, then du from column `pitch` on
+    int64_t lddy, ldgate, ldup, ld;
     int64_t rows;
     uint32_t hidden, filled, pitch;  // columns [hidden, filled) are zero
     int act;
@@ -79,7 +79,7 @@ __global__ __launch_bounds__(256) void gated_slope_kernel(GatedGradArgs a) {
             du[e] = d * value;
             if (n + e >= a.hidden) dg[e] = du[e] = 0.0f;
         }
-        uint16_t* to = a.d + r * 2 * (int64_t)a.pitch + n;
+        uint16_t* to = a.d + r * a.ld + n;
         store8<DT>(to, dg, 8u);
         store8<DT>(to + a.pitch, du, 8u);
     }
@@ -104,10 +104,10 @@ struct LossGradArgs {
     const float* lse;
     const int64_t* target;
     const uint16_t* x;
-    uint16_t* counted_x;  // [rows][width]: x, zero in rows that do not count; NULL: not wanted
+    uint16_t* counted_x;  // [rows][ldcx]: x, zero in rows that do not count; NULL: not wanted
     LossRow* row;
     float* unscale;       // what dl is to be multiplied with
-    int64_t ignore, rows, ldx;
+    int64_t ignore, rows, ldx, ldcx;
     uint32_t width, vocab;
 };
 
@@ -145,7 +145,7 @@ __global__ __launch_bounds__(256) void loss_rows_kernel(LossGradArgs a) {
             for (uint32_t n = threadIdx.x * 8u; n < a.width; n += 2048u) {
                 u32x4 v = {0, 0, 0, 0};
                 if (is) v = *(const u32x4*)(a.x + r * a.ldx + n);
-                *(u32x4*)(a.counted_x + r * (int64_t)a.width + n) = v;
+                *(u32x4*)(a.counted_x + r * a.ldcx + n) = v;
             }
     }
 }

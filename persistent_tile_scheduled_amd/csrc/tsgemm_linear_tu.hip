@@ -1,7 +1,9 @@
 // The launches of one type's kernels (-DTSG_LIN_DT=1: fp16, 2: bf16).
+#include "tsgemm_linear_few.h"
 #include "tsgemm_linear_kernel.h"
 #include "tsgemm_linear_launch.h"
 #include "tsgemm_linear_rows.h"
+#include "tsgemm_linear_shape.h"
 
 namespace tsg {
 
@@ -28,6 +30,18 @@ void LinearOf<DT>::product(LinKind kind, int tile, const LinArgs& a, hipStream_t
         case LIN_KIND_DLOGITS: return product_of<LIN_ALONG, LIN_ALONG, LIN_DLOGITS>(tile, a, s);
         case LIN_KIND_DX: return product_of<LIN_ALONG, LIN_ACROSS, LIN_OUT>(tile, a, s);
         case LIN_KIND_DW: return product_of<LIN_ACROSS, LIN_ACROSS, LIN_OUT>(tile, a, s);
+    }
+}
+
+template <>
+void LinearOf<DT>::few(LinKind kind, const LinArgs& a, hipStream_t s) {
+    const dim3 grid((unsigned)few_groups(a.N)), block(256);
+    if (kind == LIN_KIND_GATED) {
+        if (a.M <= 16u) hipLaunchKernelGGL((linear_few_kernel<DT, LIN_GATED, 1>), grid, block, 0, s, a);
+        else hipLaunchKernelGGL((linear_few_kernel<DT, LIN_GATED, 2>), grid, block, 0, s, a);
+    } else {
+        if (a.M <= 16u) hipLaunchKernelGGL((linear_few_kernel<DT, LIN_LSE, 1>), grid, block, 0, s, a);
+        else hipLaunchKernelGGL((linear_few_kernel<DT, LIN_LSE, 2>), grid, block, 0, s, a);
     }
 }
 

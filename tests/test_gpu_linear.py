@@ -13,6 +13,8 @@ pytestmark = pytest.mark.gpu
 # rows, width, hidden: one value, tiles' borders, odd ones, several tiles
 GATED = [(1, 8, 1), (1, 64, 7), (2, 4096, 130), (3, 72, 33), (16, 136, 64), (17, 128, 129), (63, 200, 65), (128, 64, 64), (129, 264, 257),
          (255, 512, 300), (256, 256, 256), (300, 520, 641)]
+# few rows, more weight rows than the workgroups take at a time
+GATED_FEW = [(1, 72, 8300), (16, 1032, 9001), (17, 520, 8200), (32, 4104, 64), (33, 4104, 64)]
 # ... with tiles of 256
 GATED_LARGE = [(2048, 64, 4096), (2049, 200, 4097)]
 
@@ -24,7 +26,7 @@ def nan(rows, width, dtype):
 @pytest.mark.parametrize("act", ACTS)
 @pytest.mark.parametrize("dtype", [FP16, BF16], ids=str)
 def test_gated_linear(dtype, act):
-    for rows, width, hidden in GATED:
+    for rows, width, hidden in GATED + GATED_FEW:
         x, wg, wu = gated_inputs(rows, width, hidden, dtype, rows + hidden)
         y, gate, up = (nan(rows, hidden, dtype) for _ in range(3))
         tsg.gated_linear(x, wg, wu, y, act, gate=gate, up=up)
@@ -79,7 +81,7 @@ LOSS = [(1, 8, 1), (1, 64, 2), (2, 72, 33), (1, 2048, 1000), (16, 136, 127), (17
 
 @pytest.mark.parametrize("dtype", [FP16, BF16], ids=str)
 def test_linear_cross_entropy(dtype):
-    for rows, width, vocab in LOSS + [(2049, 72, 8200)]:
+    for rows, width, vocab in LOSS + [(2049, 72, 8200), (3, 72, 20000), (16, 1032, 9001), (17, 136, 8200), (32, 4104, 64), (33, 4104, 64)]:
         x, w, target = loss_inputs(rows, width, vocab, dtype, rows + vocab)
         loss, lse = (torch.full((rows,), float("nan"), device=DEV) for _ in range(2))
         tsg.linear_cross_entropy(x, w, target, loss, lse)
