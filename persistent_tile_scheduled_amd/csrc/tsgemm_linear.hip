@@ -158,6 +158,7 @@ int tsgemm_gated_linear(int64_t rows, int64_t hidden, int64_t width, int dtype, 
     a.Ka = a.Kb = (uint32_t)width;
     a.y = static_cast<uint16_t*>(y); a.gate = static_cast<uint16_t*>(gate); a.up = static_cast<uint16_t*>(up);
     a.ldy = ldy; a.ldgate = ldgate; a.ldup = ldup; a.act = act;
+    a.aligned = !off(y, 16) && ldy % 8 == 0 && (!gate || (!off(gate, 16) && ldgate % 8 == 0)) && (!up || (!off(up, 16) && ldup % 8 == 0));
     (void)hipGetLastError();
     of_type(dtype, [&](auto k) {
         if (rows <= kFewRows) k.few(LIN_KIND_GATED, a, static_cast<hipStream_t>(stream));

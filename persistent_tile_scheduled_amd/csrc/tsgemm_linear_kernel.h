@@ -57,6 +57,7 @@ struct LinArgs {
     uint16_t* up;
     int64_t ldy, ldgate, ldup;
     int act;
+    int aligned;         // rows of y, gate and up begin at multiples of 16 bytes
     // LIN_LSE
     const int64_t* target;
     float2* part;        // [2 * n_blocks][M]: of half a tile's columns e and s with sum of exp(l) = 2^e s
@@ -160,12 +161,9 @@ template <int DT>
 __device__ __forceinline__ u32x4 pack8(const float* v) {
     return u32x4{pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3]), pack2<DT>(v[4], v[5]), pack2<DT>(v[6], v[7])};
 }
-// Whole chunks go past the caches (nt): y, gate and up, which nothing reads soon, would
-// evict slabs that the XCD's other workgroups are still to read (all three kept at 8192 x
-// 4096 x 8192 bf16: 2500 -> 2210 cycles a slab).
 __device__ __forceinline__ void store_some(uint16_t* to, u32x4 w, uint32_t count) {
     if (count >= 8u) {
-        __builtin_nontemporal_store((u32x4_at2)w, (u32x4_at2*)to);
+        *(u32x4_at2*)to = w;
     } else {
 #pragma unroll
         for (uint32_t e = 0; e < 7u; ++e)
@@ -554,7 +552,7 @@ __global__ __launch_bounds__(256, T == 256 ? 1 : 2) void linear_kernel(LinArgs a
 
     // Every epilogue comes in two copies: for a tile that lies inside the matrix, with
     // nothing to ask, and for one that does not.
-    const bool inside = m0 + T <= args.M && n0 + (EPI == LIN_GATED ? WT : T) <= args.N;
+    const bool inside = m0 + T <= args.M && n0 + (EPI == LIN_GATED ? WT : T) <= args.N && (EPI != LIN_GATED || args.aligned);
 
     if constexpr (EPI == LIN_GATED) {
         const Act act(args.act);
@@ -574,7 +572,14 @@ __global__ __launch_bounds__(256, T == 256 ? 1 : 2) void linear_kernel(LinArgs a
 #pragma unroll
                     for (int e = 0; e < 8; ++e) y[e] = g[e] * act_share<BELL>(act, g[e], bell) * up[e];
                     const uint32_t count = INSIDE ? 8u : m < args.M ? left(n + 32u * t, args.N) : 0u;
-                    if (INSIDE || count != 0u) {
+                    if constexpr (INSIDE) {
+                        // Past the caches (nt): y, gate and up, which nothing reads soon, would evict
+                        // slabs that the XCD's other workgroups are still to read (all three kept at
+                        // 8192 x 4096 x 8192 bf16: 2500 -> 2210 cycles a slab).
+                        __builtin_nontemporal_store(pack8<DT>(y), (u32x4*)(y_at + 32 * t));
+                        if (args.gate) __builtin_nontemporal_store(pack8<DT>(g), (u32x4*)(gate_at + 32 * t));
+                        if (args.up) __builtin_nontemporal_store(pack8<DT>(up), (u32x4*)(up_at + 32 * t));
+                    } else if (count != 0u) {
                         store8<DT>(y_at + 32 * t, y, count);
                         if (args.gate) store8<DT>(gate_at + 32 * t, g, count);
                         if (args.up) store8<DT>(up_at + 32 * t, up, count);

@@ -16,8 +16,14 @@ struct LinShape {
 
 // Tile edge (and, where the product may be split along its sum, the splits) by the
 // time they should take, in us: rounds of workgroups (one 256 x 256 tile or two 128
-// x 128 tiles per compute unit) times the slabs of one and a start, plus the
-// splits' fp32 products written and read and a second launch.
+// x 128 tiles per compute unit) times the slabs of one (1.1 of a large tile, 1.3 where
+// few share what they read; of a small one 0.7 alone and 1.0 beside another) and a start
+// of 4, plus the splits' fp32 products written and read at 6 TB/s and a second launch.
+// Measured with both sides of each choice, bf16, the activation's gradient (about 10)
+// included: dx 2000 x 2048, hidden 2048: large tiles in 1, 2 and 4 splits 94, 67 and 57,
+// small ones in 1 and 2 63 and 55; dx 1000 x 2504, hidden 6001: large in 4, 6 and 8 splits
+// 98, 85 and 118, small in 3 90; 512 x 512, hidden 1024: small in 1, 4 and 8 33, 19.2 and
+// 19.2; the projection 2000 x 2048 x 2048 large 40.6, small 32.0.
 // `columns`: of the product per tile edge T, T or (two projections) T / 2.
 inline LinShape linear_shape(int64_t M, int64_t N, int64_t slabs, bool halves, bool may_split) {
     constexpr int64_t kCus = 256;  // MI355X
@@ -29,10 +35,10 @@ inline LinShape linear_shape(int64_t M, int64_t N, int64_t slabs, bool halves, b
         for (int64_t splits = 1, per = slabs; splits <= 64; splits = (slabs + per - 2) / (per - 1)) {
             per = (slabs + splits - 1) / splits;
             if (splits > 1 && tiles * splits > 2 * room) break;
-            const double slab_us = tile == 256 ? 1.2 : tiles * splits <= kCus ? 0.45 : 0.8;
+            const double slab_us = tile == 256 ? (tiles * splits <= kCus / 2 ? 1.3 : 1.1) : tiles * splits <= kCus ? 0.7 : 1.0;
             const double rounds = (double)((tiles * splits + room - 1) / room);
-            const double product = 8e-6 * (double)(M * N) / 4.0 + 0.03;
-            const double us = rounds * ((double)per * slab_us + 3.0) + (splits > 1 ? 3.0 + (double)splits * product : 0.0);
+            const double product = 8e-6 * (double)(M * N) / 6.0 + 0.03;
+            const double us = rounds * ((double)per * slab_us + 4.0) + (splits > 1 ? 3.0 + (double)splits * product : 0.0);
             if (best.tile == 0 || us < best_us) {
                 best = {tile, mb, nb, slabs, splits, per};
                 best_us = us;
