@@ -271,6 +271,8 @@ __global__ __launch_bounds__(256, T == 256 ? 1 : 2) void linear_kernel(LinArgs a
     const uint32_t first_unit = worker_of_workgroup(blockIdx.x, workers, 8u, workers);
     uint32_t ld_unit = first_unit, ld_slab = 0, ld_end = 0, ld_event = 0, ld_m = 0, ld_n = 0;
     uint32_t a_dec = 0, b_dec = 0;
+    const uint64_t a_step = A_ALONG ? BK * 2u : (uint64_t)BK * lda * 2u;
+    uint64_t b_step = B_ALONG ? BK * 2u : (uint64_t)BK * ldb * 2u;
     i32x4 ra, rb;
     auto seek = [&]() __attribute__((always_inline)) {
         if (ld_slab == ld_end && ld_unit < units) {
@@ -298,6 +300,15 @@ __global__ __launch_bounds__(256, T == 256 ? 1 : 2) void linear_kernel(LinArgs a
             a_dec = b_dec = 0u;
             ld_event = 0xFFFFFFFFu;
         }
+        if constexpr (EPI == LIN_OUT && A_ALONG) {  // the halves' weights may lie differently
+            const uint32_t ld = second ? (uint32_t)args.ldb2 : (uint32_t)args.ldb;
+            b_step = (uint64_t)BK * ld * 2u;
+#pragma unroll
+            for (int q = 0; q < ND; ++q) {
+                const uint32_t at = (wave * ND + q) * 64u + lane, across = at / (T / 8);
+                voff[ND + q] = (across & 15u) * ld * 2u + ((at % (T / 8)) ^ swz_b(across)) * 16u;
+            }
+        }
         if constexpr (A_ALONG || B_ALONG) {
             const uint32_t past = k0 + k_chunk * 8u >= K ? 0x80000000u : 0u;
 #pragma unroll
@@ -308,7 +319,6 @@ __global__ __launch_bounds__(256, T == 256 ? 1 : 2) void linear_kernel(LinArgs a
     };
     const uint32_t dma_first = lds_base + wave * ND * 1024u;
     uint32_t dma_lds = dma_first;
-    const uint64_t a_step = A_ALONG ? BK * 2u : (uint64_t)BK * lda * 2u, b_step = B_ALONG ? BK * 2u : (uint64_t)BK * ldb * 2u;
     auto add64 = [](i32x4& r, uint64_t d) __attribute__((always_inline)) {
         const uint64_t a = (((uint64_t)(uint32_t)r.y) << 32 | (uint32_t)r.x) + d;  // stride bits are 0
         r.x = (int)(uint32_t)a;
