@@ -202,6 +202,40 @@ __device__ __forceinline__ LinUnit lin_unit(const LinArgs& args, uint32_t unit) 
     return u;
 }
 
+// The reads of a phase by gaps: gap s holds reads first[s] ... first[s + 1] - 1.
+template <int STEPS>
+struct LinReads {
+    int first[STEPS + 1];
+};
+// `per` reads a gap, `lead` reads of the operand that is needed first from gap `start` on,
+// then `rest` of the other: `space` gaps apart (0: as they come), or, `row_reads` != 0, each
+// `row_reads` of them once their row of `row_steps` MFMAs is used up.
+template <int STEPS>
+constexpr LinReads<STEPS> lin_reads(int per, int lead, int rest, int start, int space, int row_reads, int row_steps) {
+    LinReads<STEPS> t = {};
+    int gap = start, count = 0, at = 0;
+    for (int i = 0; i < lead + rest; ++i) {
+        int from = start;
+        if (i >= lead && space != 0) from = start + (lead + per - 1) / per + (i - lead) * space / per;
+        if (i >= lead && row_reads != 0) from = (i - lead) / row_reads * row_steps + row_steps - 1 + kGap;
+        if (gap < from) {
+            gap = from;
+            count = 0;
+        }
+        if (count == per) {
+            ++gap;
+            count = 0;
+        }
+        if (gap >= STEPS) break;
+        while (at <= gap) t.first[at++] = i;
+        ++count;
+        if (at <= STEPS) t.first[at] = i + 1;
+    }
+    const int all = t.first[at <= STEPS ? at : STEPS];
+    while (at <= STEPS) t.first[at++] = all;
+    return t;
+}
+
 // acc = a * b, in the registers that acc is in: with an output of its own the
 // accumulator of a tile's first slab could be another register than that of the
 // others, and the copies between them would lie right beside MFMAs that the compiler
@@ -425,29 +459,13 @@ __global__ __launch_bounds__(256, T == 256 ? 1 : 2) void linear_kernel(LinArgs a
     constexpr int LATE = DF < NL ? START + (NL - 1 - DF) * SPACE + 1 : 0;     // phase 1: gap after its DMAs
     constexpr int STEP_AT = DF < NL ? LATE : START + (DF - 1) * SPACE + 1;    // the loader's step, in phase 1 or 2
     static_assert(STEP_AT + PIECES <= STEPS, "the loader's step needs gaps");
-    // The gap of each LDS read of a phase, in order: PER a gap and none before what it
-    // overwrites is used up.  One a gap where there are gaps enough: the four waves' reads
-    // of 8 bytes a lane fill the LDS's time of one MFMA.
-    constexpr int PER = T == 256 ? 1 : 2, LATER = T == 256 ? 2 : 1;
-    constexpr auto read_gap = [](int phase, int op) constexpr {
-        int gap = START, count = 0;
-        for (int i = 0;; ++i) {
-            int from = START;
-            if (phase == 1 && i >= RA) from = START + (RA + PER - 1) / PER + (i - RA) * LATER / PER;  // the second half of B: for phase 2
-            if (phase == 2 && i >= RB) from = ((i - RB) / (2 * RA / F)) * F + F - 1 + kGap;              // A: a row of blocks once it is used up
-            if (gap < from) {
-                gap = from;
-                count = 0;
-            }
-            if (count == PER) {
-                ++gap;
-                count = 0;
-            }
-            if (i == op) return gap;
-            ++count;
-        }
-    };
-    static_assert(read_gap(1, RA + RB - 1) < STEPS && read_gap(2, RA + RB - 1) < STEPS, "every read needs a gap");
+    // Which LDS reads of a phase go into which gap, in order: one a gap (T = 256; the four
+    // waves' reads of 8 bytes a lane fill the LDS's time of one MFMA) or two, and none before
+    // what it overwrites is used up.
+    using Reads = LinReads<STEPS>;
+    constexpr Reads reads1 = lin_reads<STEPS>(T == 256 ? 1 : 2, RA, RB, START, T == 256 ? 2 : 1, 0, 0);
+    constexpr Reads reads2 = lin_reads<STEPS>(T == 256 ? 1 : 2, RB, RA, START, 0, 2 * RA / F, F);
+    static_assert(reads1.first[STEPS] == RA + RB && reads2.first[STEPS] == RA + RB, "every read needs a gap");
     using I0 = std::integral_constant<int, 0>;
     using I1 = std::integral_constant<int, 1>;
     using TRUE_ = std::integral_constant<bool, true>;
@@ -475,15 +493,14 @@ __global__ __launch_bounds__(256, T == 256 ? 1 : 2) void linear_kernel(LinArgs a
                 constexpr int i = s - START;
                 if constexpr (SECOND ? i % SPACE == 0 && i / SPACE < DF : i % SPACE == 0 && i / SPACE < NL - DF)
                     dma_op(std::integral_constant<int, (SECOND ? 0 : DF) + i / SPACE>{});
-                static_for<0, RA + RB>([&](auto r_c) __attribute__((always_inline)) {
-                    constexpr int r = decltype(r_c)::value;
-                    if constexpr (read_gap(SECOND ? 2 : 1, r) == s) {
+                static_for<SECOND ? reads2.first[s] : reads1.first[s], SECOND ? reads2.first[s + 1] : reads1.first[s + 1]>(
+                    [&](auto r_c) __attribute__((always_inline)) {
+                        constexpr int r = decltype(r_c)::value;
                         if constexpr (SECOND && r < RB) read_b(I0{}, r_c);
                         else if constexpr (SECOND) read_a(I0{}, std::integral_constant<int, r - RB>{});
                         else if constexpr (r < RA) read_a(I1{}, r_c);
                         else read_b(I1{}, std::integral_constant<int, r - RA>{});
-                    }
-                });
+                    });
             }
             if constexpr (SECOND == (DF == NL) && s >= STEP_AT && s < STEP_AT + PIECES) step(std::integral_constant<int, s - STEP_AT>{});
             if constexpr (s + 1 >= START) {
