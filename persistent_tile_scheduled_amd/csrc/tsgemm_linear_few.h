@@ -8,10 +8,10 @@
 // a lane and row, the next 128 values' loads on their way while these are multiplied
 // (16x16x32 MFMA, x's rows past the last read as zeros).
 //
-// Measured bf16: one row, 4096 x 8192 (two weights, 134 MB) 24.0 us, 5.6 TB/s with part of
-// them in the Infinity Cache; 16 rows, 4096 x 131072 (1.07 GB) 240 us, 4.5 TB/s (the tile
-// kernel 60 and 239).  Loads that stream past the caches (nt) 26.3 and 265; 256 values a
-// turn 26.6 and 243; twice the workgroups 24.0 and 240.
+// Measured bf16: one row, 4096 x 8192 (two weights, 134 MB) 26.5 us, 5.1 TB/s; 16 rows,
+// 4096 x 131072 (1.07 GB) 239 us, 4.5 TB/s (the tile kernel 60 and 239).  Two sets of the
+// first one's weights in turn, half of them in the Infinity Cache, 24.0 us; loads past the
+// caches (nt) 26.3 and 265, 256 values a turn 26.6 and 243, twice the workgroups 24.0 and 240.
 #pragma once
 
 #include "tsgemm_linear_kernel.h"

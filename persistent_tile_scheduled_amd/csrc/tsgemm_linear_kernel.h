@@ -20,6 +20,15 @@
 // and columns past a matrix's end, and the sum's last slab past its end, read
 // zeros: a wave's descriptor ends with the matrix, and of rows along the sum the
 // lanes past the end ask for an address that no descriptor covers.
+//
+// Workgroups are persistent: the loader runs two slabs ahead and on into the next
+// tile, so that its first slabs arrive during the epilogue.  Measured bf16, T = 256, in
+// cycles a slab (its 128 MFMAs take 2048) and of the epilogue: logsumexp 2190 and 11660,
+// gated 2190 and 9450 (three outputs 2210 and 20000), dx 2200 and 8360, dW 2490 and 8450.
+// 8192 x 4096 x 131072: loss 5.55 ms, 1584 TFLOP/s, gradient 17.9 ms, 1472; gated 8192 x
+// 4096 x 16384 with both projections kept 1.56 ms, 1405, gradient 3.31 ms, 1329 (the
+// library's plain product of 8192^3 1619, 1388 with b across the sum, 1204 with both):
+// bound by the board's power.
 #pragma once
 
 #include "tile_scheduler.h"
