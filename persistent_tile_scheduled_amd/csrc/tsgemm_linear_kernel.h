@@ -117,7 +117,8 @@ __device__ __forceinline__ void lin_pause(uint32_t& state) {
 // The activations are g p(g), with p the logistic function of z = g (c + k g^2)
 // (silu: c = 1, k = 0; gelu by tanh: (1 + tanh(z / 2)) / 2 is the logistic function of
 // z) or, BELL, the normal distribution function (gelu).  Both without a branch: an
-// accumulator that lives across one is copied.
+// accumulator that lives across one is copied.  g^2 ends at 1e30, where z has long
+// run past every exponential: past fp32's end it would make silu's k g^2 0 * inf.
 struct Act {
     float c, k;  // times log2 e
     __device__ __forceinline__ explicit Act(int act)
@@ -140,6 +141,7 @@ __device__ __forceinline__ float tail_over_bell(float a) {
     h = __builtin_fmaf(h, t, 0.11962586641311646f);
     return h * t;
 }
+__device__ __forceinline__ float act_square(float g) { return fminf(g * g, 1e30f); }
 // p(g); `bell` receives exp(-g^2 / 2) (BELL)
 template <bool BELL>
 __device__ __forceinline__ float act_share(const Act& k, float g, float& bell) {
@@ -148,7 +150,7 @@ __device__ __forceinline__ float act_share(const Act& k, float g, float& bell) {
         const float tail = bell * tail_over_bell(fabsf(g));
         return g < 0.0f ? tail : 1.0f - tail;
     } else {
-        return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-g * __builtin_fmaf(k.k, g * g, k.c)));
+        return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-g * __builtin_fmaf(k.k, act_square(g), k.c)));
     }
 }
 

@@ -37,7 +37,7 @@ __device__ __forceinline__ void act_slope(const Act& k, float g, float& value, f
         slope = __builtin_fmaf(g * 0.39894228f, bell, p);
     } else {
         // p (1 - p) z'; where p has run out of fp32 the slope is 0 or 1, not 0 * inf
-        const float rise = p * (1.0f - p) * __builtin_fmaf(3.0f * k.k, g * g, k.c) * (1.0f / kLog2e);
+        const float rise = p * (1.0f - p) * __builtin_fmaf(3.0f * k.k, act_square(g), k.c) * (1.0f / kLog2e);
         slope = p == 0.0f || p == 1.0f ? p : __builtin_fmaf(g, rise, p);
     }
 }
