@@ -347,9 +347,9 @@ int tsgemm_mx_weight_grad(int64_t rows, int64_t out, int64_t width, int dtype, i
  *   with x[rows][width], gate_weight and up_weight[hidden][width], y[rows][hidden];
  *   act is TSGEMM_SILU (g / (1 + exp(-g))), TSGEMM_GELU (g times the normal
  *   distribution function) or TSGEMM_GELU_TANH (its approximation by tanh).  g and
- *   u are fp32 until y is rounded.  gate and up (each may be NULL: not kept) are g
- *   and u rounded to dtype, what the gradient reads.  rows * hidden == 0 launches
- *   nothing. */
+ *   u are fp32 until y is rounded; act(inf) is inf, act(-inf) a NaN.  gate and up (each
+ *   may be NULL: not kept) are g and u rounded to dtype, what the gradient reads.
+ *   rows * hidden == 0 launches nothing. */
 enum { TSGEMM_SILU = 1, TSGEMM_GELU = 2, TSGEMM_GELU_TANH = 3 };
 int tsgemm_gated_linear(int64_t rows, int64_t hidden, int64_t width, int dtype, int act, const void* x, int64_t ldx,
                         const void* gate_weight, int64_t ldgw, const void* up_weight, int64_t lduw, void* y, int64_t ldy,
@@ -361,6 +361,7 @@ int tsgemm_gated_linear(int64_t rows, int64_t hidden, int64_t width, int dtype, 
  *     dgate_weight = dg^T * x      dup_weight = du^T * x
  *   dg and du are rounded to dtype, as the gradients of a 16-bit tensor are (in
  *   fp16 a value past 65504 is an infinity), before the products sum them in fp32.
+ *   An infinite gate stands for a far one: act(-inf) is 0, its slopes are 0 and 1.
  *   dx may be NULL, or dgate_weight and dup_weight together (not wanted).
  *   `workspace` is 16-byte aligned, of at least tsgemm_gated_linear_grad_workspace
  *   bytes, contents irrelevant.  Without rows the weights' gradients are zero,

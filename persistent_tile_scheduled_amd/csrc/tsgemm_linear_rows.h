@@ -27,16 +27,18 @@ struct GatedGradArgs {
     int act;
 };
 
-// act(g) = g p(g) and its derivative p + g p'.
+// act(g) = g p(g) and its derivative p + g p'.  Where p or the bell has run out of fp32
+// they are what they tend to, 0 and g, 0 and 1: not 0 * inf, of a gate that was kept as an
+// infinity (fp16: any from 65520 on).
 template <bool BELL>
 __device__ __forceinline__ void act_slope(const Act& k, float g, float& value, float& slope) {
     float bell;
     const float p = act_share<BELL>(k, g, bell);
-    value = g * p;
+    value = p == 0.0f ? 0.0f : g * p;
     if constexpr (BELL) {
-        slope = __builtin_fmaf(g * 0.39894228f, bell, p);
+        slope = bell == 0.0f ? p : __builtin_fmaf(g * 0.39894228f, bell, p);
     } else {
-        // p (1 - p) z'; where p has run out of fp32 the slope is 0 or 1, not 0 * inf
+        // p (1 - p) z'
         const float rise = p * (1.0f - p) * __builtin_fmaf(3.0f * k.k, act_square(g), k.c) * (1.0f / kLog2e);
         slope = p == 0.0f || p == 1.0f ? p : __builtin_fmaf(g, rise, p);
     }

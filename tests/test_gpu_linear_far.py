@@ -1,11 +1,11 @@
 """The gated projection and its gradient where a projection is far out: past 2^64, whose
-square fp32 does not hold, and (forward) infinite.  Bounds: linear_cases.py."""
+square fp32 does not hold, and infinite.  Bounds: linear_cases.py."""
 
 import pytest
 import torch
 
 import persistent_tile_scheduled_amd as tsg
-from tests.linear_cases import ACTS, BF16, DEV, act64, check_gated_grad, gated_inputs, half, randn
+from tests.linear_cases import ACTS, BF16, DEV, FP16, act64, check_gated_grad, gated_inputs, half, randn
 
 pytestmark = pytest.mark.gpu
 
@@ -54,3 +54,26 @@ def test_far_gates(act):
     dx, dwg, dwu = (torch.full(t.shape, float("nan"), dtype=BF16, device=DEV) for t in (x, wg, wu))
     tsg.gated_linear_grad(dy, x, wg, wu, gate, up, dx, dwg, dwu, act)
     check_gated_grad(dy, x, wg, wu, gate, up, act, dx, dwg, dwu, "far gates")
+
+
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("dtype", [FP16, BF16], ids=str)
+def test_infinite_gates(dtype, act):
+    """An infinite gate, which fp16 keeps of a g from 65520 on, stands for a far one: act(-inf) is 0,
+    the slopes are 0 and 1.  The same bits as from gates of 1e4 to either side, where act and slope
+    have ended, but for the sums that hold dy act(inf)."""
+    rows, width, hidden = 40, 64, 70
+    x, wg, wu = gated_inputs(rows, width, hidden, dtype, 32)
+    dy, gate, up = randn(1, rows, hidden).to(dtype), randn(2, rows, hidden, scale=2).to(dtype), randn(3, rows, hidden).to(dtype)
+    near = gate.clone()
+    for at, g in (((3, 5), -1.0), ((8, 5), -1.0), ((9, 69), -1.0), ((7, 9), 1.0)):
+        gate[at], near[at] = g * float("inf"), g * 1e4
+    got, want = ([torch.full(t.shape, float("nan"), dtype=dtype, device=DEV) for t in (x, wg, wu)] for _ in range(2))
+    tsg.gated_linear_grad(dy, x, wg, wu, gate, up, *got, act)
+    tsg.gated_linear_grad(dy, x, wg, wu, near, up, *want, act)
+    check_gated_grad(dy, x, wg, wu, near, up, act, *want, "near")
+    assert torch.equal(got[1], want[1])
+    for i, at in ((0, 7), (2, 9)):
+        assert not torch.isfinite(got[i][at]).any()
+        got[i][at] = want[i][at]
+        assert torch.equal(got[i], want[i])
