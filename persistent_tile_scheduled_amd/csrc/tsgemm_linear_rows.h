@@ -113,11 +113,11 @@ struct LossGradArgs {
     uint32_t width, vocab;
 };
 
-// What the gradient needs of every row.  dl is held over the largest |dloss| of the
-// rows that count, so that of a loss's mean over the rows, all of whose dloss are
-// alike, no rounding of dloss itself enters; fp16, which has few exponents, holds 2^13
-// times that, and its least normal value stands for 2^-27 of the largest.  Every
-// workgroup finds that largest value for itself.
+// What the gradient needs of every row.  dl is held over the largest finite |dloss| of
+// the rows that count (an infinite one is its own row's matter), so that of a loss's mean
+// over the rows, all of whose dloss are alike, no rounding of dloss itself enters; fp16,
+// which has few exponents, holds 2^13 times that, and its least normal value stands for
+// 2^-27 of the largest.  Every workgroup finds that largest value for itself.
 template <int DT>
 __global__ __launch_bounds__(256) void loss_rows_kernel(LossGradArgs a) {
     __shared__ float most[4];
@@ -128,13 +128,16 @@ __global__ __launch_bounds__(256) void loss_rows_kernel(LossGradArgs a) {
     constexpr float kMore = DT == DT_FP16 ? 8192.0f : 1.0f;
     float top = 0.0f;
     for (int64_t r = threadIdx.x; r < a.rows; r += 256)
-        if (counts(r)) top = fmaxf(top, fabsf(a.dloss[r]));
+        if (counts(r)) {
+            const float d = fabsf(a.dloss[r]);
+            top = d < __builtin_inff() ? fmaxf(top, d) : top;
+        }
 #pragma unroll
     for (int d = 1; d < 64; d *= 2) top = fmaxf(top, __shfl_xor(top, d));
     if ((threadIdx.x & 63u) == 0u) most[threadIdx.x >> 6] = top;
     __syncthreads();
     top = fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3]));
-    if (!(top >= 0x1p-110f && top < __builtin_inff())) top = 1.0f;  // no scale comes of it
+    if (!(top >= 0x1p-110f)) top = 1.0f;  // no scale comes of it
     if (blockIdx.x == 0 && threadIdx.x == 0) *a.unscale = top / kMore;
     for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
         const bool is = counts(r);
