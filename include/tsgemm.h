@@ -392,8 +392,9 @@ int tsgemm_linear_cross_entropy(int64_t rows, int64_t vocab, int64_t width, int 
  *   whatever x, lse and dloss hold there: its dl is zero, and dweight has no term of
  *   it.  The logits are formed again, piece by piece of the vocabulary; of a piece
  *   dl is held in `workspace`, over the largest finite |dloss| (in fp16 over 2^-13 of
- *   it) and rounded to dtype; dx and dweight are multiplied with that in fp32.  dx or
- *   dweight may be NULL (not wanted).  rows == 0 makes dweight zero. */
+ *   it) and rounded to dtype; dx and dweight are multiplied with that in fp32, so over
+ *   it their sums have to fit fp32 too.  dx or dweight may be NULL (not wanted).
+ *   rows == 0 makes dweight zero. */
 int64_t tsgemm_linear_cross_entropy_grad_workspace(int64_t rows, int64_t vocab, int64_t width);
 int tsgemm_linear_cross_entropy_grad(int64_t rows, int64_t vocab, int64_t width, int dtype, const float* dloss, const void* x,
                                      int64_t ldx, const void* weight, int64_t ldw, const int64_t* target,

@@ -127,9 +127,9 @@ __global__ __launch_bounds__(256, EPI == LIN_GATED && MB == 2 ? 1 : 2) void line
                 const float l = total(b, 0);
                 if (r < M && c < N) {
                     if (target[b] == (int64_t)c) args.hit[r] = l;
-                    // the sum is in units of 2^top
-                    const float e = l * kLog2e, now = fmaxf(top[b], e), base = now == -__builtin_inff() ? 0.0f : now;
-                    sum[b] = sum[b] * __builtin_amdgcn_exp2f(top[b] - base) + __builtin_amdgcn_exp2f(__builtin_fmaf(l, kLog2e, -base));
+                    // the sum is in units of exp(top)
+                    const float now = fmaxf(top[b], l), base = now == -__builtin_inff() ? 0.0f : now;
+                    sum[b] = sum[b] * exp_past(top[b], base) + exp_past(l, base);
                     top[b] = now;
                 }
             }
@@ -163,7 +163,7 @@ __global__ __launch_bounds__(256, EPI == LIN_GATED && MB == 2 ? 1 : 2) void line
             float all = top[b];
 #pragma unroll
             for (int d = 1; d < 16; d *= 2) all = fmaxf(all, __shfl_xor(all, d));
-            float s = sum[b] * __builtin_amdgcn_exp2f(top[b] - (all == -__builtin_inff() ? 0.0f : all));
+            float s = sum[b] * exp_past(top[b], all == -__builtin_inff() ? 0.0f : all);
 #pragma unroll
             for (int d = 1; d < 16; d *= 2) s += __shfl_xor(s, d);
             if (n == 0u && m + 16u * b < M) args.part[(size_t)blockIdx.x * M + m + 16u * b] = make_float2(all, s);

@@ -40,12 +40,17 @@ typedef uint32_t u32x4_at2 __attribute__((ext_vector_type(4), aligned(2)));  // 
 
 constexpr float kLog2e = 1.44269504f;
 
+// exp(v - from).  The difference comes first: v log2 e - from log2 e in one fma, an
+// instruction less, carries the rounding of the second term, which past logits of 3e9 is
+// more than an exponential has room for (8192 x 4096 x 131072 bf16 loss 5953 us, so 5984).
+__device__ __forceinline__ float exp_past(float v, float from) { return __builtin_amdgcn_exp2f((v - from) * kLog2e); }
+
 enum { LIN_ALONG = 0, LIN_ACROSS = 1 };  // an operand's layout: the sum's index fastest, or slowest
 enum { LIN_GATED = 0, LIN_LSE = 1, LIN_DLOGITS = 2, LIN_OUT = 3 };
 
 // What the cross entropy's gradient needs of a row.
 struct LossRow {
-    float lse2;      // its logsumexp times log2 e
+    float lse;       // its logsumexp
     float d;         // its share of the gradient, times the scale of dl
     int32_t target;  // -1: the row does not count
     int32_t unused;
@@ -69,7 +74,7 @@ struct LinArgs {
     int aligned;         // rows of y, gate and up begin at multiples of 16 bytes
     // LIN_LSE
     const int64_t* target;
-    float2* part;        // [2 * n_blocks][M]: of half a tile's columns e and s with sum of exp(l) = 2^e s
+    float2* part;        // [2 * n_blocks][M]: of half a tile's columns t and s with sum of exp(l) = exp(t) s
     float* hit;          // [M]: the target's logit
     // LIN_DLOGITS
     const LossRow* row;
@@ -628,8 +633,8 @@ __global__ __launch_bounds__(256, T == 256 ? 1 : 2) void linear_kernel(LinArgs a
         if (args.act == kActBell) inside ? gated(TRUE_{}, TRUE_{}) : gated(TRUE_{}, FALSE_{});
         else inside ? gated(FALSE_{}, TRUE_{}) : gated(FALSE_{}, FALSE_{});
     } else if constexpr (EPI == LIN_LSE) {
-        // Every lane's sum is of powers of 2 relative to its own largest logit; the four
-        // lanes of a row meet afterwards, all rows at once.
+        // Every lane's sum is relative to its own largest logit; the four lanes of a row
+        // meet afterwards, all rows at once.
         float top[F], sum[F];
         const uint32_t c0 = n0 + wc * WT;
         auto sums = [&](auto inside_c) __attribute__((always_inline)) {
@@ -656,15 +661,15 @@ __global__ __launch_bounds__(256, T == 256 ? 1 : 2) void linear_kernel(LinArgs a
                         b = fmaxf(fmaxf(b, v[t][e + 2]), v[t][e + 3]);
                     }
                 a = fmaxf(a, b);
-                top[fm] = a == -__builtin_inff() ? a : a * kLog2e;
-                const float from = a == -__builtin_inff() ? 0.0f : a * kLog2e;  // the sum is in units of 2^from
+                top[fm] = a;
+                const float from = a == -__builtin_inff() ? 0.0f : a;  // the sum is in units of exp(from)
                 float s0 = 0.0f, s1 = 0.0f;
 #pragma unroll
                 for (int t = 0; t < F / 2; ++t)
 #pragma unroll
                     for (int e = 0; e < 8; e += 2) {
-                        s0 += __builtin_amdgcn_exp2f(__builtin_fmaf(v[t][e], kLog2e, -from));
-                        s1 += __builtin_amdgcn_exp2f(__builtin_fmaf(v[t][e + 1], kLog2e, -from));
+                        s0 += exp_past(v[t][e], from);
+                        s1 += exp_past(v[t][e + 1], from);
                     }
                 sum[fm] = s0 + s1;
                 __builtin_amdgcn_sched_barrier(0);  // one row of blocks after the other: they do not fit the registers
@@ -692,7 +697,7 @@ __global__ __launch_bounds__(256, T == 256 ? 1 : 2) void linear_kernel(LinArgs a
 #pragma unroll
         for (int fm = 0; fm < F; ++fm) {
             const float all = max_over_groups(top[fm]);
-            const float s = sum_over_groups(sum[fm] * __builtin_amdgcn_exp2f(top[fm] - (all == -__builtin_inff() ? 0.0f : all)));
+            const float s = sum_over_groups(sum[fm] * exp_past(top[fm], all == -__builtin_inff() ? 0.0f : all));
             const uint32_t m = row_of(fm);
             if (lg == 0u && m < args.M) args.part[(size_t)(u.n_idx * 2u + wc) * args.M + m] = make_float2(all, s);
         }
@@ -713,7 +718,7 @@ __global__ __launch_bounds__(256, T == 256 ? 1 : 2) void linear_kernel(LinArgs a
                     float v[8];
                     eight(fm, t, v);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) v[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(v[e], kLog2e, -r.lse2));
+                    for (int e = 0; e < 8; ++e) v[e] = exp_past(v[e], r.lse);
                     if (some) {
 #pragma unroll
                         for (uint32_t e = 0; e < 8; ++e) v[e] -= at == 32u * t + 8u * lg + e ? 1.0f : 0.0f;

@@ -91,7 +91,7 @@ __global__ __launch_bounds__(256) void gated_slope_kernel(GatedGradArgs a) {
 // cross entropy
 // ---------------------------------------------------------------------------
 struct LossArgs {
-    const float2* part;  // [parts][rows]: e and s
+    const float2* part;  // [parts][rows]: t and s
     const float* hit;
     const int64_t* target;
     float* loss;
@@ -143,7 +143,7 @@ __global__ __launch_bounds__(256) void loss_rows_kernel(LossGradArgs a) {
         const bool is = counts(r);
         if (threadIdx.x == 0) {
             LossRow row = {0.0f, 0.0f, -1, 0};
-            if (is) row = {a.lse[r] * kLog2e, a.dloss[r] / top * kMore, (int32_t)a.target[r], 0};
+            if (is) row = {a.lse[r], a.dloss[r] / top * kMore, (int32_t)a.target[r], 0};
             a.row[r] = row;
         }
         if (a.counted_x)

@@ -65,7 +65,7 @@ void LinearOf<DT>::loss_rows(const LossGradArgs& a, hipStream_t s) {
 }
 
 #if TSG_LIN_DT == 1  // what no type goes by
-// 16 rows a workgroup, 64 threads a row: sum of 2^e s over the parts, each thread's
+// 16 rows a workgroup, 64 threads a row: sum of exp(t) s over the parts, each thread's
 // over every 64th part, eight requested at a time, then over the threads in order.
 __global__ __launch_bounds__(1024) void loss_join_kernel(LossArgs a) {
     __shared__ float tops[64][16], sums[64][16];
@@ -83,9 +83,9 @@ __global__ __launch_bounds__(1024) void loss_join_kernel(LossArgs a) {
 #pragma unroll
             for (int k = 0; k < 8; ++k) t = fmaxf(t, v[k].x);
             const float from = zero_if_none(t);
-            sum *= __builtin_amdgcn_exp2f(top - from);
+            sum *= exp_past(top, from);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) sum += v[k].y * __builtin_amdgcn_exp2f(v[k].x - from);
+            for (int k = 0; k < 8; ++k) sum += v[k].y * exp_past(v[k].x, from);
             top = t;
         }
     }
@@ -96,10 +96,9 @@ __global__ __launch_bounds__(1024) void loss_join_kernel(LossArgs a) {
     for (int k = 1; k < 64; ++k) top = fmaxf(top, tops[k][i]);
     const float from = zero_if_none(top);
     sum = 0.0f;
-    for (int k = 0; k < 64; ++k) sum += sums[k][i] * __builtin_amdgcn_exp2f(tops[k][i] - from);
-    // in fp64, divided by what the logits were multiplied with: the loss is the
-    // difference of two numbers that may be close
-    const double lse = (double)from / (double)kLog2e + log((double)sum);
+    for (int k = 0; k < 64; ++k) sum += sums[k][i] * exp_past(tops[k][i], from);
+    // in fp64: the loss is the difference of two numbers that may be close
+    const double lse = (double)from + log((double)sum);
     a.lse[r] = (float)lse;
     const int64_t t = a.target[r];
     a.loss[r] = t == a.ignore ? 0.0f : t >= 0 && t < (int64_t)a.vocab ? (float)(lse - (double)a.hit[r]) : __builtin_nanf("");

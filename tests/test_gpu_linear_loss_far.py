@@ -1,10 +1,11 @@
-"""The linear head's cross entropy and its gradient with infinities: in dloss.  Bounds: linear_cases.py."""
+"""The linear head's cross entropy and its gradient with infinities in dloss, and with
+logits as far out as fp32 goes.  Bounds: linear_cases.py."""
 
 import pytest
 import torch
 
 import persistent_tile_scheduled_amd as tsg
-from tests.linear_cases import BF16, DEV, FP16, check_loss_grad, loss64, loss_inputs, randn
+from tests.linear_cases import BF16, DEV, FP16, U, check_loss_grad, half, loss64, loss_inputs, randn
 
 pytestmark = pytest.mark.gpu
 DTYPES = pytest.mark.parametrize("dtype", [FP16, BF16], ids=str)
@@ -34,3 +35,55 @@ def test_a_dloss_that_is_no_number_stays_in_its_row(dtype, others, bad):
     assert not torch.isfinite(dx[5]).any() and not torch.isfinite(dw[target[5]]).any()
     rest = torch.arange(rows, device=DEV) != 5
     assert torch.equal(dx[rest], want[rest])
+
+
+# type, x[:, 0] and the size of w[:, 0]: logits of up to their product, all of one sign or of both
+FAR = [(FP16, 1.0, 6e4), (FP16, 6e4, 6e4), (BF16, 1.0, 1e5), (BF16, 1.0, 1e9), (BF16, 1.0, 1e12), (BF16, 1.0, 1e30), (BF16, 1.0, 3e38)]
+
+
+def far_logits(dtype, x0, size, signs, rows, vocab):
+    """Exact logits x0 w[:, 0] (the other values are zeros), the two largest of them alike."""
+    x, w = torch.zeros((rows, 8), dtype=dtype, device=DEV), torch.zeros((vocab, 8), dtype=dtype, device=DEV)
+    v = size * (0.1 + 0.9 * torch.rand(vocab, generator=torch.Generator().manual_seed(7)).to(DEV))
+    w[:, 0] = {"+": 1, "-": -1, "+-": 1 - 2 * (torch.arange(vocab, device=DEV) % 2)}[signs] * v
+    top = w[:, 0].argmax()
+    w[(top + 2) % vocab] = w[top]
+    x[:, 0] = x0
+    target = torch.arange(rows, device=DEV) * 37 % vocab
+    target[::3] = top
+    return x, w, target
+
+
+@pytest.mark.parametrize("signs", ["+", "-", "+-"])
+@pytest.mark.parametrize("rows", [5, 30, 100, 600])
+def test_far_logits(rows, signs):
+    """lse is off by its exponentials' sum, 2^-17, and its rounding; the gradient, which goes by that
+    lse, by 2^-18 p, its rounding of dl and the sums'.  Apart from those, what is below 2^-126, the least
+    normal value of fp32 and bf16, may be 0: exp of a difference past -88 is.  The sums are formed over
+    the largest |dloss|, 0.25, and multiplied with it afterwards: where their terms over it pass fp32's
+    3.4e38 (weights of 3e38 alone) dx may be infinite."""
+    vocab = 515
+    for dtype, x0, size in FAR:
+        x, w, target = far_logits(dtype, x0, size, signs, rows, vocab)
+        l = x.double() @ w.double().t()
+        want, hit = torch.logsumexp(l, dim=1), l.gather(1, target[:, None])[:, 0]
+        loss, lse = nan(rows), nan(rows)
+        tsg.linear_cross_entropy(x, w, target, loss, lse)
+        assert torch.isfinite(lse).all(), (dtype, x0, size)
+        assert ((lse - want).abs() <= 2.0 ** -17 + 2 * U * want.abs()).all(), (dtype, x0, size)
+        fits = want - hit < 3e38
+        assert ((loss - (want - hit)).abs() <= 2.0 ** -17 + 2 * U * (want - hit).abs())[fits].all(), (dtype, x0, size)
+        e, dloss = half(dtype), torch.full((rows,), 0.25, device=DEV)
+        dx, dw = nan(rows, 8, dtype=dtype), nan(vocab, 8, dtype=dtype)
+        tsg.linear_cross_entropy_grad(dloss, x, w, target, lse, dx, dw)
+        p = torch.exp(l - lse.double()[:, None])
+        dl = 0.25 * p
+        off = 2.0 ** -20 * p
+        dl[torch.arange(rows, device=DEV), target] -= 0.25
+        off = off + (e + 2.0 ** -20) * dl.abs() + (2.0 ** -39 if dtype == FP16 else 2.0 ** -126)
+        tiny = 2.0 ** -25 if dtype == FP16 else 2.0 ** -126
+        for got, a, b in ((dx, (dl, off), w.double()), (dw, (dl.t(), off.t()), x.double())):
+            ref = a[0] @ b
+            bound = e * ref.abs() + (a[1] + 2 * (a[0].shape[1] + 64) * U * a[0].abs()) @ b.abs() + tiny
+            there = (ref.abs() < 0.99 * torch.finfo(dtype).max) & (a[0].abs() @ b.abs() / 0.25 < 3.4e38)
+            assert ((got - ref).abs() <= bound)[there].all(), (dtype, x0, size)
