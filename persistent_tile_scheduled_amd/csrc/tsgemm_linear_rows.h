@@ -169,26 +169,27 @@ struct LinSumArgs {
 };
 template <int DT>
 __global__ __launch_bounds__(256) void linear_sum_kernel(LinSumArgs a) {
-    const uint64_t i = ((uint64_t)blockIdx.x * 256u + threadIdx.x) * 8u, count = (uint64_t)a.M * a.N;
-    if (i >= count) return;
-    const uint32_t m = (uint32_t)(i / a.N), n = (uint32_t)(i % a.N);
-    const bool upper = m >= a.half;
-    const uint32_t mo = upper ? m - a.half : m;
-    if (mo >= a.out_rows) return;
-    f32x4 x = {0.f, 0.f, 0.f, 0.f}, y = x;
-#pragma unroll 4
-    for (uint32_t s = 0; s < a.splits; ++s) {
-        x += *(const f32x4*)(a.sums + s * count + i);
-        y += *(const f32x4*)(a.sums + s * count + i + 4);
-    }
+    const uint64_t count = (uint64_t)a.M * a.N;
     const float scale = a.unscale ? *a.unscale : 1.0f;
-    float v[8];
+    for (uint64_t i = ((uint64_t)blockIdx.x * 256u + threadIdx.x) * 8u; i < count; i += (uint64_t)gridDim.x * 2048u) {
+        const uint32_t m = (uint32_t)(i / a.N), n = (uint32_t)(i % a.N);
+        const bool upper = m >= a.half;
+        const uint32_t mo = upper ? m - a.half : m;
+        if (mo >= a.out_rows) continue;
+        f32x4 x = {0.f, 0.f, 0.f, 0.f}, y = x;
+#pragma unroll 4
+        for (uint32_t s = 0; s < a.splits; ++s) {
+            x += *(const f32x4*)(a.sums + s * count + i);
+            y += *(const f32x4*)(a.sums + s * count + i + 4);
+        }
+        float v[8];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        v[e] = x[e] * scale;
-        v[4 + e] = y[e] * scale;
+        for (int e = 0; e < 4; ++e) {
+            v[e] = x[e] * scale;
+            v[4 + e] = y[e] * scale;
+        }
+        store8<DT>((upper ? a.out2 + (int64_t)mo * a.ldo2 : a.out + (int64_t)mo * a.ldo) + n, v, 8u);
     }
-    store8<DT>((upper ? a.out2 + (int64_t)mo * a.ldo2 : a.out + (int64_t)mo * a.ldo) + n, v, 8u);
 }
 
 }  // namespace tsg

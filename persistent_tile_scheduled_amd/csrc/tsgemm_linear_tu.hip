@@ -12,6 +12,10 @@ namespace {
 constexpr int DT = TSG_LIN_DT;
 constexpr uint32_t kCus = 256;  // MI355X
 
+// Workgroups of a kernel that goes on to further work by the grid's size: 2^32 threads
+// or more are not launched whole (the runtime counts them in 32 bits, without an error).
+int64_t at_most(int64_t groups, int64_t most) { return groups < most ? groups : most; }
+
 template <int AL, int BL, int EPI>
 void product_of(int tile, const LinArgs& a, hipStream_t s) {
     const uint32_t units = a.m_blocks * a.n_blocks * a.splits, room = tile == 256 ? kCus : 2u * kCus;
@@ -47,21 +51,21 @@ void LinearOf<DT>::few(LinKind kind, const LinArgs& a, hipStream_t s) {
 
 template <>
 void LinearOf<DT>::sum(const LinSumArgs& a, hipStream_t s) {
-    const uint64_t count = (uint64_t)a.M * a.N / 8u;
-    hipLaunchKernelGGL(linear_sum_kernel<DT>, dim3((unsigned)((count + 255u) / 256u)), dim3(256), 0, s, a);
+    const int64_t count = (int64_t)a.M * a.N / 8;
+    hipLaunchKernelGGL(linear_sum_kernel<DT>, dim3((unsigned)at_most((count + 255) / 256, 1 << 20)), dim3(256), 0, s, a);
 }
 
 template <>
 void LinearOf<DT>::gated_slope(const GatedGradArgs& a, hipStream_t s) {
-    const uint64_t groups = (uint64_t)a.rows * ((a.filled / 8u + 255u) / 256u);
-    const dim3 grid((unsigned)(groups < 4096u ? groups : 4096u)), block(256);
+    const int64_t groups = a.rows * (int64_t)((a.filled / 8u + 255u) / 256u);
+    const dim3 grid((unsigned)at_most(groups, 4096)), block(256);
     if (a.act == kActBell) hipLaunchKernelGGL((gated_slope_kernel<DT, true>), grid, block, 0, s, a);
     else hipLaunchKernelGGL((gated_slope_kernel<DT, false>), grid, block, 0, s, a);
 }
 
 template <>
 void LinearOf<DT>::loss_rows(const LossGradArgs& a, hipStream_t s) {
-    hipLaunchKernelGGL(loss_rows_kernel<DT>, dim3((unsigned)(a.rows < 1024 ? a.rows : 1024)), dim3(256), 0, s, a);
+    hipLaunchKernelGGL(loss_rows_kernel<DT>, dim3((unsigned)at_most(a.rows, 1024)), dim3(256), 0, s, a);
 }
 
 #if TSG_LIN_DT == 1  // what no type goes by
@@ -70,38 +74,41 @@ void LinearOf<DT>::loss_rows(const LossGradArgs& a, hipStream_t s) {
 __global__ __launch_bounds__(1024) void loss_join_kernel(LossArgs a) {
     __shared__ float tops[64][16], sums[64][16];
     const uint32_t i = threadIdx.x & 15u, j = threadIdx.x >> 4;
-    const int64_t r = (int64_t)blockIdx.x * 16 + i;
     const auto zero_if_none = [](float e) { return e == -__builtin_inff() ? 0.0f : e; };
-    float top = -__builtin_inff(), sum = 0.0f;
-    if (r < a.rows) {
-        for (uint32_t p = j; p < a.parts; p += 512u) {
-            float2 v[8];
-            float t = top;
+    for (int64_t first = (int64_t)blockIdx.x * 16; first < a.rows; first += (int64_t)gridDim.x * 16) {
+        const int64_t r = first + i;
+        float top = -__builtin_inff(), sum = 0.0f;
+        if (r < a.rows) {
+            for (uint32_t p = j; p < a.parts; p += 512u) {
+                float2 v[8];
+                float t = top;
 #pragma unroll
-            for (uint32_t k = 0; k < 8; ++k)
-                v[k] = p + 64u * k < a.parts ? a.part[(size_t)(p + 64u * k) * a.rows + r] : make_float2(-__builtin_inff(), 0.0f);
+                for (uint32_t k = 0; k < 8; ++k)
+                    v[k] = p + 64u * k < a.parts ? a.part[(size_t)(p + 64u * k) * a.rows + r] : make_float2(-__builtin_inff(), 0.0f);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) t = fmaxf(t, v[k].x);
-            const float from = zero_if_none(t);
-            sum *= exp_past(top, from);
+                for (int k = 0; k < 8; ++k) t = fmaxf(t, v[k].x);
+                const float from = zero_if_none(t);
+                sum *= exp_past(top, from);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) sum += v[k].y * exp_past(v[k].x, from);
-            top = t;
+                for (int k = 0; k < 8; ++k) sum += v[k].y * exp_past(v[k].x, from);
+                top = t;
+            }
         }
+        __syncthreads();  // the rows before have been read
+        tops[j][i] = top;
+        sums[j][i] = sum;
+        __syncthreads();
+        if (j != 0u || r >= a.rows) continue;
+        for (int k = 1; k < 64; ++k) top = fmaxf(top, tops[k][i]);
+        const float from = zero_if_none(top);
+        sum = 0.0f;
+        for (int k = 0; k < 64; ++k) sum += sums[k][i] * exp_past(tops[k][i], from);
+        // in fp64: the loss is the difference of two numbers that may be close
+        const double lse = (double)from + log((double)sum);
+        a.lse[r] = (float)lse;
+        const int64_t t = a.target[r];
+        a.loss[r] = t == a.ignore ? 0.0f : t >= 0 && t < (int64_t)a.vocab ? (float)(lse - (double)a.hit[r]) : __builtin_nanf("");
     }
-    tops[j][i] = top;
-    sums[j][i] = sum;
-    __syncthreads();
-    if (j != 0u || r >= a.rows) return;
-    for (int k = 1; k < 64; ++k) top = fmaxf(top, tops[k][i]);
-    const float from = zero_if_none(top);
-    sum = 0.0f;
-    for (int k = 0; k < 64; ++k) sum += sums[k][i] * exp_past(tops[k][i], from);
-    // in fp64: the loss is the difference of two numbers that may be close
-    const double lse = (double)from + log((double)sum);
-    a.lse[r] = (float)lse;
-    const int64_t t = a.target[r];
-    a.loss[r] = t == a.ignore ? 0.0f : t >= 0 && t < (int64_t)a.vocab ? (float)(lse - (double)a.hit[r]) : __builtin_nanf("");
 }
 
 // dweight = 0 of a call without rows
@@ -111,11 +118,11 @@ __global__ __launch_bounds__(256) void linear_zero_kernel(uint16_t* out, int64_t
 }
 
 void launch_loss_join(const LossArgs& a, hipStream_t s) {
-    hipLaunchKernelGGL(loss_join_kernel, dim3((unsigned)((a.rows + 15) / 16)), dim3(1024), 0, s, a);
+    hipLaunchKernelGGL(loss_join_kernel, dim3((unsigned)at_most((a.rows + 15) / 16, 1 << 16)), dim3(1024), 0, s, a);
 }
 
 void launch_linear_zero(uint16_t* out, int64_t ld, int64_t rows, uint32_t width, hipStream_t s) {
-    hipLaunchKernelGGL(linear_zero_kernel, dim3((unsigned)(rows < 4096 ? rows : 4096)), dim3(256), 0, s, out, ld, rows, width);
+    hipLaunchKernelGGL(linear_zero_kernel, dim3((unsigned)at_most(rows, 4096)), dim3(256), 0, s, out, ld, rows, width);
 }
 #endif
 
