@@ -787,16 +787,16 @@ __global__ __launch_bounds__(1024) void layer_norm_grad_wide_kernel(LnGradArgs a
     }
 }
 
-// dgamma and dbeta from the workgroups' sums: 32 columns per workgroup, 4 per
+// dgamma and dbeta from the workgroups' sums: 32 columns per workgroup from `first` on, 4 per
 // lane, so that a wave reads 8 workgroups' sums at once; the lanes' and the 16
 // waves' shares meet in a fixed order.  `groups` may be 0 (no rows): the
 // gradients are then 0.
 template <int WDT>
 __global__ __launch_bounds__(1024) void layer_norm_grad_sum_kernel(const float* part, uint32_t groups, uint32_t pitch,
-                                                                   uint32_t width, void* dgamma, void* dbeta) {
+                                                                   uint32_t first, uint32_t width, void* dgamma, void* dbeta) {
     __shared__ float sums[2][16][32];
     const uint32_t lane = threadIdx.x & 63u, wave = threadIdx.x >> 6;
-    const uint32_t c = blockIdx.x * 32u + (lane & 7u) * 4u;
+    const uint32_t c = first + blockIdx.x * 32u + (lane & 7u) * 4u;
     f32x4 s[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
     if (c < pitch) {
 #pragma unroll 4
@@ -817,7 +817,7 @@ __global__ __launch_bounds__(1024) void layer_norm_grad_sum_kernel(const float* 
         }
     lds_barrier();
     if (threadIdx.x < 64u) {
-        const uint32_t k = threadIdx.x >> 5, at = blockIdx.x * 32u + (threadIdx.x & 31u);
+        const uint32_t k = threadIdx.x >> 5, at = first + blockIdx.x * 32u + (threadIdx.x & 31u);
         float v = 0.f;
 #pragma unroll
         for (int w = 0; w < 16; ++w) v += sums[k][w][threadIdx.x & 31u];

@@ -152,13 +152,19 @@ void launch_layer_norm_grad(int dt, const LnGradArgs& args, hipStream_t s) {
 
 void launch_layer_norm_grad_sum(int wdt, const float* part, uint32_t groups, uint32_t pitch, uint32_t width, void* dgamma,
                                 void* dbeta, hipStream_t s) {
-    const dim3 grid((width + 31u) / 32u), block(1024);
-    if (wdt == DT_FP16)
-        hipLaunchKernelGGL((layer_norm_grad_sum_kernel<DT_FP16>), grid, block, 0, s, part, groups, pitch, width, dgamma, dbeta);
-    else if (wdt == DT_BF16)
-        hipLaunchKernelGGL((layer_norm_grad_sum_kernel<DT_BF16>), grid, block, 0, s, part, groups, pitch, width, dgamma, dbeta);
-    else
-        hipLaunchKernelGGL((layer_norm_grad_sum_kernel<DT_FP32>), grid, block, 0, s, part, groups, pitch, width, dgamma, dbeta);
+    // A launch has less than 2^32 threads (the runtime counts them in 32 bits and cuts what
+    // is more without an error): 32 for a column.
+    constexpr uint32_t kMost = 1u << 26;
+    for (int64_t at = 0; at < (int64_t)width; at += kMost) {
+        const uint32_t first = (uint32_t)at, columns = width - first < kMost ? width - first : kMost;
+        const dim3 grid((columns + 31u) / 32u), block(1024);
+        if (wdt == DT_FP16)
+            hipLaunchKernelGGL((layer_norm_grad_sum_kernel<DT_FP16>), grid, block, 0, s, part, groups, pitch, first, width, dgamma, dbeta);
+        else if (wdt == DT_BF16)
+            hipLaunchKernelGGL((layer_norm_grad_sum_kernel<DT_BF16>), grid, block, 0, s, part, groups, pitch, first, width, dgamma, dbeta);
+        else
+            hipLaunchKernelGGL((layer_norm_grad_sum_kernel<DT_FP32>), grid, block, 0, s, part, groups, pitch, first, width, dgamma, dbeta);
+    }
 }
 
 void launch_mx_quantize(int dt, const void* x, int64_t ld, int64_t rows, uint32_t width, uint8_t* codes, uint8_t* scales,
