@@ -25,8 +25,14 @@ namespace tsg {
 
 // C = 0 when K == 0 (an empty sum): plain 16-byte stores, N % 8 == 0.
 __global__ void tsgemm_zero_kernel(uint16_t* C, int64_t count8) {
-    const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-    if (i < count8) *(u32x4*)(C + 8 * i) = u32x4{0u, 0u, 0u, 0u};
+    const int64_t step = (int64_t)gridDim.x * blockDim.x;
+    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < count8; i += step) *(u32x4*)(C + 8 * i) = u32x4{0u, 0u, 0u, 0u};
+}
+// C = 0, of count8 times 8 values; a launch of 2^32 threads would be cut without an error
+// (the runtime counts them in 32 bits)
+static void launch_zero(uint16_t* C, int64_t count8, hipStream_t s) {
+    const int64_t blocks = (count8 + 255) / 256, most = int64_t(1) << 20;
+    hipLaunchKernelGGL(tsgemm_zero_kernel, dim3((unsigned)(blocks < most ? blocks : most)), dim3(256), 0, s, C, count8);
 }
 
 // Schedule dump: the same scheduler and worker numbering as the GEMM kernel.
@@ -255,10 +261,7 @@ int run_impl(const tsgemm_plan* p, const void* A, const void* B, void* C, void* 
     (void)hipGetLastError();
     if (p->k_blocks == 0) {
         // empty sum: C = 0 (N % 8 == 0, so 8 elements per thread)
-        const int64_t count8 = p->M * p->N / 8;
-        const unsigned blocks = (unsigned)((count8 + 255) / 256);
-        hipLaunchKernelGGL(tsg::tsgemm_zero_kernel, dim3(blocks), dim3(256), 0,
-                           static_cast<hipStream_t>(stream), a.C, count8);
+        tsg::launch_zero(a.C, p->M * p->N / 8, static_cast<hipStream_t>(stream));
     } else {
         p->kernel->fn(a, g.P, static_cast<hipStream_t>(stream));
     }
@@ -294,10 +297,7 @@ int run_mx_impl(const tsgemm_plan* p, const void* A, const void* SFA, const void
     if (rc != TSGEMM_OK) return rc;
     (void)hipGetLastError();
     if (p->k_blocks == 0) {
-        const int64_t count8 = p->M * p->N / 8;
-        const unsigned blocks = (unsigned)((count8 + 255) / 256);
-        hipLaunchKernelGGL(tsg::tsgemm_zero_kernel, dim3(blocks), dim3(256), 0,
-                           static_cast<hipStream_t>(stream), static_cast<uint16_t*>(C), count8);
+        tsg::launch_zero(static_cast<uint16_t*>(C), p->M * p->N / 8, static_cast<hipStream_t>(stream));
     } else {
         tsg::MxArgs a;
         a.A = static_cast<const uint8_t*>(A);
