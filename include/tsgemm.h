@@ -377,8 +377,10 @@ int tsgemm_gated_linear_grad(int64_t rows, int64_t hidden, int64_t width, int dt
  *     l = x * weight^T    lse = log(sum_v exp(l[v]))    loss = lse - l[target]
  *   per row, with x[rows][width], weight[vocab][width], target int64[rows], loss
  *   and lse fp32[rows].  A row whose target is ignore_index has loss 0; one whose
- *   target is neither that nor in [0, vocab) has a NaN loss.  An infinite or NaN
- *   logit makes its row's loss and lse NaN.  vocab >= 1; rows == 0 launches nothing.
+ *   target is neither that nor in [0, vocab) has a NaN loss.  A logit of inf or NaN makes
+ *   its row's loss and lse NaN.  One of -inf adds nothing; as the target's its loss is
+ *   inf, and a row of them alone has an lse of -inf and a NaN loss.  vocab >= 1;
+ *   rows == 0 launches nothing.
  *   `workspace` as above, tsgemm_linear_cross_entropy_workspace bytes. */
 int64_t tsgemm_linear_cross_entropy_workspace(int64_t rows, int64_t vocab, int64_t width);
 int tsgemm_linear_cross_entropy(int64_t rows, int64_t vocab, int64_t width, int dtype, const void* x, int64_t ldx,

@@ -1,11 +1,11 @@
-"""The linear head's cross entropy and its gradient with infinities in dloss, and with
-logits as far out as fp32 goes.  Bounds: linear_cases.py."""
+"""The linear head's cross entropy and its gradient with infinities in dloss and in
+single logits, and with logits as far out as fp32 goes.  Bounds: linear_cases.py."""
 
 import pytest
 import torch
 
 import persistent_tile_scheduled_amd as tsg
-from tests.linear_cases import BF16, DEV, FP16, U, check_loss_grad, half, loss64, loss_inputs, randn
+from tests.linear_cases import BF16, DEV, FP16, U, check_loss, check_loss_grad, half, loss64, loss_inputs, randn
 
 pytestmark = pytest.mark.gpu
 DTYPES = pytest.mark.parametrize("dtype", [FP16, BF16], ids=str)
@@ -35,6 +35,42 @@ def test_a_dloss_that_is_no_number_stays_in_its_row(dtype, others, bad):
     assert not torch.isfinite(dx[5]).any() and not torch.isfinite(dw[target[5]]).any()
     rest = torch.arange(rows, device=DEV) != 5
     assert torch.equal(dx[rest], want[rest])
+
+
+@DTYPES
+@pytest.mark.parametrize("rows", [16, 30, 100, 600])
+def test_infinite_logits(dtype, rows):
+    """x[:, 0] is 1, so a weight of -inf there is a logit of -inf: its exponential is 0 and the row
+    is that of the other words; the loss of such a target is inf.  A logit of inf makes a row NaN, a
+    row of nothing but -inf has an lse of -inf and no loss."""
+    width, vocab = 64, 515
+    x, w, target = loss_inputs(rows, width, vocab, dtype, 43, ignored=0.1)
+    x[:, 0] = 1.0
+    out = torch.arange(vocab, device=DEV) % 3 == 1
+    w[out, 0] = -INF
+    keep = torch.nonzero(~out)[:, 0]
+    at = torch.full((vocab,), -7, device=DEV)      # of no word that is left
+    at[keep] = torch.arange(len(keep), device=DEV)
+    counted = target != -100
+    gone = counted & out[target.clamp_min(0)]
+    assert gone.any() and (counted & ~gone).any()
+    moved = torch.where(counted & ~gone, at[target.clamp_min(0)], -100)
+    loss, lse = nan(rows), nan(rows)
+    tsg.linear_cross_entropy(x, w, target, loss, lse)
+    assert (loss[gone] == INF).all()
+    check_loss(x, w[keep], moved, torch.where(gone, 0.0, loss), lse, "-inf here and there")
+    dloss, dw = torch.where(gone, 0.0, randn(1, rows)), nan(vocab, width, dtype=dtype)
+    masked = torch.where(gone, -100, target)
+    tsg.linear_cross_entropy_grad(dloss, x, w, masked, lse, dweight=dw)
+    check_loss_grad(dloss, x, w[keep], moved, lse, None, dw[keep], "-inf here and there")
+    assert not dw[out].any()
+    x[3, 0] = -1.0                                  # ... of inf
+    tsg.linear_cross_entropy(x, w, target, loss, lse)
+    assert torch.isnan(lse[3]) and (torch.isnan(loss[3]) if counted[3] else loss[3] == 0) and torch.isfinite(lse).sum() == rows - 1
+    x[3, 0] = 1.0
+    w[:, 0] = -INF
+    tsg.linear_cross_entropy(x, w, target, loss, lse)
+    assert (lse == -INF).all() and torch.isnan(loss[counted]).all() and not loss[~counted].any()
 
 
 # type, x[:, 0] and the size of w[:, 0]: logits of up to their product, all of one sign or of both
