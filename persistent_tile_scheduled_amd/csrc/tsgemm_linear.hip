@@ -87,10 +87,12 @@ struct GatedGradPlan {
 
 struct LossPlan {
     LinShape s;
+    bool few;
     int64_t parts, hit, bytes;
     LossPlan(int64_t rows, int64_t vocab, int64_t width) {
         s = linear_shape(rows, vocab, slabs_of(width), false, false);
-        parts = rows <= kFewRows ? few_groups(vocab) : 2 * s.n_blocks;
+        few = takes_few(s, rows, vocab, width, 1);
+        parts = few ? few_groups(vocab) : 2 * s.n_blocks;
         hit = aligned(parts * rows * 8);
         bytes = hit + aligned(rows * 4);
     }
@@ -161,7 +163,7 @@ int tsgemm_gated_linear(int64_t rows, int64_t hidden, int64_t width, int dtype, 
     a.aligned = !off(y, 16) && ldy % 8 == 0 && (!gate || (!off(gate, 16) && ldgate % 8 == 0)) && (!up || (!off(up, 16) && ldup % 8 == 0));
     (void)hipGetLastError();
     of_type(dtype, [&](auto k) {
-        if (rows <= kFewRows) k.few(LIN_KIND_GATED, a, static_cast<hipStream_t>(stream));
+        if (takes_few(s, rows, hidden, width, 2)) k.few(LIN_KIND_GATED, a, static_cast<hipStream_t>(stream));
         else k.product(LIN_KIND_GATED, s.tile, a, static_cast<hipStream_t>(stream));
     });
     return launched("gated linear");
@@ -313,7 +315,7 @@ int tsgemm_linear_cross_entropy(int64_t rows, int64_t vocab, int64_t width, int 
     a.hit = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + plan.hit);
     (void)hipGetLastError();
     of_type(dtype, [&](auto k) {
-        if (rows <= kFewRows) k.few(LIN_KIND_LSE, a, s);
+        if (plan.few) k.few(LIN_KIND_LSE, a, s);
         else k.product(LIN_KIND_LSE, plan.s.tile, a, s);
     });
     rc = launched("linear cross entropy");

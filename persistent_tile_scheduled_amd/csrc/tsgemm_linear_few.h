@@ -1,6 +1,6 @@
 // The gated projection and the cross entropy's sums for few rows (up to 32), for
 // gfx950 (CDNA4): every weight is read once and used for all rows, so the weights'
-// bytes are the time.
+// bytes are the time while there are few.
 //
 // A workgroup of 4 waves takes 16 weight rows (16 of each weight of the gated
 // projection) at a time; the waves share the sum, 128 values of it each in turn, and
@@ -9,9 +9,11 @@
 // (16x16x32 MFMA, x's rows past the last read as zeros).
 //
 // Measured bf16: one row, 4096 x 8192 (two weights, 134 MB) 26.5 us, 5.1 TB/s; 16 rows,
-// 4096 x 131072 (1.07 GB) 239 us, 4.5 TB/s (the tile kernel 60 and 239).  Two sets of the
-// first one's weights in turn, half of them in the Infinity Cache, 24.0 us; loads past the
-// caches (nt) 26.3 and 265, 256 values a turn 26.6 and 243, twice the workgroups 24.0 and 240.
+// 4096 x 131072 (1.07 GB) 239 us, 4.5 TB/s, of 1, 8 and 32 rows 174, 196 and 352 (takes_few of
+// tsgemm_linear_shape.h says when the tile kernel, 240 there, is taken).  With two sets of
+// the first one's weights in turn, half of them in the Infinity Cache, 24.0 and 239 us; in
+// that set-up loads past the caches (nt) take 26.3 and 265, 256 values a turn 26.6 and 243,
+// twice the workgroups 24.0 and 240.
 #pragma once
 
 #include "tsgemm_linear_kernel.h"

@@ -19,7 +19,7 @@ enum LinKind { LIN_KIND_GATED, LIN_KIND_LSE, LIN_KIND_DLOGITS, LIN_KIND_DX, LIN_
 template <int DT>
 struct LinearOf {
     static void product(LinKind kind, int tile, const LinArgs& a, hipStream_t s);
-    static void few(LinKind kind, const LinArgs& a, hipStream_t s);  // LIN_KIND_GATED, LIN_KIND_LSE up to kFewRows rows
+    static void few(LinKind kind, const LinArgs& a, hipStream_t s);  // LIN_KIND_GATED, LIN_KIND_LSE where takes_few
     static void sum(const LinSumArgs& a, hipStream_t s);
     static void gated_slope(const GatedGradArgs& a, hipStream_t s);
     static void loss_rows(const LossGradArgs& a, hipStream_t s);

@@ -12,6 +12,7 @@ namespace tsg {
 struct LinShape {
     int tile;
     int64_t m_blocks, n_blocks, slabs, splits, per_split;
+    double us;  // by the rule below
 };
 
 // Tile edge (and, where the product may be split along its sum, the splits) by the
@@ -28,7 +29,6 @@ struct LinShape {
 inline LinShape linear_shape(int64_t M, int64_t N, int64_t slabs, bool halves, bool may_split) {
     constexpr int64_t kCus = 256;  // MI355X
     LinShape best = {};
-    double best_us = 0;
     for (int tile : {256, 128}) {
         const int64_t cols = halves ? tile / 2 : tile;
         const int64_t mb = (M + tile - 1) / tile, nb = (N + cols - 1) / cols, tiles = mb * nb, room = tile == 256 ? kCus : 2 * kCus;
@@ -39,20 +39,33 @@ inline LinShape linear_shape(int64_t M, int64_t N, int64_t slabs, bool halves, b
             const double rounds = (double)((tiles * splits + room - 1) / room);
             const double product = 8e-6 * (double)(M * N) / 6.0 + 0.03;
             const double us = rounds * ((double)per * slab_us + 4.0) + (splits > 1 ? 3.0 + (double)splits * product : 0.0);
-            if (best.tile == 0 || us < best_us) {
-                best = {tile, mb, nb, slabs, splits, per};
-                best_us = us;
-            }
+            if (best.tile == 0 || us < best.us) best = {tile, mb, nb, slabs, splits, per, us};
             if (!may_split || per <= 1) break;
         }
     }
     return best;
 }
 
-// Up to this many rows the weights' way through the chip is all the time there is:
-// the kernel for few rows (tsgemm_linear_few.h) then takes the products that read x
-// and the weights alone, in `few_groups` workgroups.
+// Up to this many rows there is a kernel (tsgemm_linear_few.h) for the products that read
+// x and the weights alone, in `few_groups` workgroups.
 constexpr int64_t kFewRows = 32;
+
+// Whether it takes a product: by the time that either kernel should take, in us.  A million
+// values of the weights are 0.30 there and every row 0.008 on top (0.0042 where two weights
+// share it), as each group of 16 weight rows fetches x for itself; the tile kernel pays
+// none for rows up to 128, but 0.38 a million (the weights' way through the chip), and at
+// least 1.2 of the rule above.  Measured bf16, weights from HBM, few and tile: cross
+// entropy 4096 x 8192 of 1 and 32 rows 20.7 and 62, 32 and 63; 4096 x 131072 of 1, 16, 17
+// and 32 rows 174 and 240, 239 and 241, 267 and 241, 352 and 242; 1000 x 50001 of 8 and 24
+// rows 28 and 35, 38 and 36; gated 4096 x 14336 of 1 and 32 rows 45 and 67, 65 and 67; 1024
+// x 65536 of 1 and 32 rows 44 and 49, 67 and 50.  Of 189 such shapes the rule's choice is
+// on average 0.5% slower than the better one, at worst 17%; always this kernel 6% and 79%.
+inline bool takes_few(const LinShape& s, int64_t rows, int64_t columns, int64_t width, int weights) {
+    const double values = 1e-6 * (double)weights * (double)columns * (double)width;
+    const double few = values * (0.30 + (weights == 2 ? 0.0042 : 0.008) * (double)rows);
+    const double tile = 1.2 * s.us > 0.38 * values ? 1.2 * s.us : 0.38 * values;
+    return rows <= kFewRows && few < tile;
+}
 inline int64_t few_groups(int64_t columns) {
     const int64_t tiles = (columns + 15) / 16;
     return tiles < 512 ? tiles : 512;

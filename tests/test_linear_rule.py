@@ -1,38 +1,11 @@
 """The rules that choose pieces of the vocabulary and splits of the sum for the gradient of
-the linear head's cross entropy, from their own source, and the workspaces that follow."""
-
-import ctypes
-import functools
-import os
-import subprocess
-import tempfile
+the linear head's cross entropy, and the kernel for few rows, from their own source, and
+the workspaces that follow."""
 
 import pytest
 
 import persistent_tile_scheduled_amd as tsg
-from persistent_tile_scheduled_amd import _build
-
-_SHIM = """
-#include "tsgemm_linear_shape.h"
-extern "C" int64_t piece(int64_t rows, int64_t vocab) { return tsg::vocab_piece(rows, vocab); }
-extern "C" void shape(int64_t M, int64_t N, int64_t slabs, int halves, int may_split, int64_t* a) {
-    const tsg::LinShape s = tsg::linear_shape(M, N, slabs, halves != 0, may_split != 0);
-    a[0] = s.tile; a[1] = s.m_blocks; a[2] = s.n_blocks; a[3] = s.splits; a[4] = s.per_split;
-}
-"""
-
-
-@functools.cache
-def _lib():
-    with tempfile.TemporaryDirectory() as d:
-        out = os.path.join(d, "rule.so")
-        subprocess.run(["g++", "-O1", "-std=c++17", "-shared", "-fPIC", "-x", "c++", "-", "-I", _build.CSRC, "-o", out],
-                       input=_SHIM, text=True, check=True)
-        lib = ctypes.CDLL(out)
-    lib.piece.argtypes, lib.piece.restype = [ctypes.c_int64] * 2, ctypes.c_int64
-    lib.shape.argtypes = [ctypes.c_int64] * 3 + [ctypes.c_int] * 2 + [ctypes.POINTER(ctypes.c_int64)]
-    return lib
-
+from tests.linear_rule import FEW, TILE, linear_shape, takes_few, vocab_piece
 
 MIB = 1 << 20
 
@@ -41,7 +14,7 @@ MIB = 1 << 20
 def test_a_piece_of_the_vocabulary_takes_128_mib(rows):
     """... or 2048 columns where those take more; whole tiles that cover the vocabulary, of one size."""
     for vocab in (1, 255, 257, 2100, 5003, 50001, 131072, 1 << 22, (1 << 22) + 1, 1 << 27):
-        p = _lib().piece(rows, vocab)
+        p = vocab_piece(rows, vocab)
         assert p % 256 == 0 and 2 * rows * p <= max(128 * MIB, 4096 * rows, 512 * rows)
         pieces = -(-vocab // p)
         assert p <= 1 << 22 and (pieces == 1 or p - (vocab - (pieces - 1) * p) < 256 * pieces)
@@ -61,12 +34,37 @@ def test_the_gradients_workspace_is_far_below_the_logits_gradient(rows, vocab, w
 
 
 def test_splits_are_as_few_as_that():
-    a = (ctypes.c_int64 * 5)()
     for M in (1, 33, 300, 512, 2000, 8192, 50000):
         for N in (8, 264, 1000, 2504, 8192):
             for slabs in (1, 2, 9, 64, 189, 2048):
-                _lib().shape(M, N, slabs, 0, 1, a)
-                tile, mb, nb, splits, per = a
+                tile, mb, nb, splits, per = linear_shape(M, N, slabs, False, True)
                 assert (mb - 1) * tile < M <= mb * tile and (nb - 1) * tile < N <= nb * tile
                 assert (splits - 1) * per < slabs <= splits * per  # every split has slabs
                 assert splits == 1 or mb * nb * splits <= (512 if tile == 256 else 1024)
+
+
+@pytest.mark.parametrize("weights", [1, 2])
+def test_the_kernel_for_few_rows(weights):
+    """Never above 32 rows, always for one token; of more rows and wider products no more of them."""
+    for width in (8, 512, 4096, 8192):
+        for columns in (1, 1000, 8192, 50001, 131072):
+            takes = [takes_few(rows, columns, width, weights) for rows in range(1, 40)]
+            assert takes[0] and not any(takes[32:])
+            assert takes == sorted(takes, reverse=True), (width, columns)
+
+
+@pytest.mark.parametrize("shapes,few", [(FEW, True), (TILE, False)])
+def test_the_gpu_tests_shapes_take_the_kernels_they_are_for(shapes, few):
+    for weights, rows, width, columns in shapes:
+        assert takes_few(rows, columns, width, weights) == few, (weights, rows, width, columns)
+
+
+@pytest.mark.parametrize("rows", [16, 32])
+def test_the_workspace_is_that_of_either_kernel(rows):
+    """Parts of 8 bytes a row: 512 workgroups', or two a tile of 256 or 128 columns."""
+    for vocab, width in ((5003, 4096), (131072, 512), (200000, 4096)):
+        few = takes_few(rows, vocab, width, 1)
+        tile, _, nb, _, _ = linear_shape(rows, vocab, -(-width // 64), False, False)
+        parts = min(512, -(-vocab // 16)) if few else 2 * nb
+        up = lambda n: -(-n // 256) * 256  # noqa: E731
+        assert tsg.linear_cross_entropy_workspace(rows, vocab, width) == up(8 * parts * rows) + up(4 * rows)
