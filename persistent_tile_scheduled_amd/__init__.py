@@ -471,6 +471,8 @@ def _row_stride(name, t, rows, width):
 
 def _matrix(name, t, shape, dtype, dev):
     """Pointer and row stride of another matrix of the call."""
+    if t is None:
+        raise ValueError(f"{name} must be given")
     if t.shape != shape or t.dtype != dtype or t.get_device() != dev:
         raise ValueError(f"{name} must be a {dtype} tensor of shape {tuple(shape)} on CUDA device {dev}")
     return t.data_ptr(), _row_stride(name, t, shape[0], shape[1])
@@ -654,6 +656,8 @@ def _act_code(act):
 
 def _x_16bit(x):
     """dtype and its code, rows, width, device index and row stride of the activation x."""
+    if x is None:
+        raise ValueError("x must be given")
     dt = _dtype_code("x", x.dtype)
     if dt == FP32:
         raise ValueError(f"x must be float16 or bfloat16, got {x.dtype}")
@@ -666,6 +670,8 @@ def _maybe_matrix(name, t, shape, dtype, dev):
 
 def _weight(name, t, width, dtype, dev):
     """Rows, pointer and row stride of a weight."""
+    if t is None:
+        raise ValueError(f"{name} must be given")
     if t.dim() != 2:
         raise ValueError(f"{name} must have two dimensions")
     return (t.shape[0],) + _matrix(name, t, (t.shape[0], width), dtype, dev)
