@@ -23,12 +23,13 @@
 //
 // Workgroups are persistent: the loader runs two slabs ahead and on into the next
 // tile, so that its first slabs arrive during the epilogue.  Measured bf16, T = 256, in
-// cycles a slab (its 128 MFMAs take 2048) and of the epilogue: logsumexp 2190 and 11660,
-// gated 2190 and 9450 (three outputs 2210 and 20000), dx 2200 and 8360, dW 2490 and 8450.
-// 8192 x 4096 x 131072: loss 5.55 ms, 1584 TFLOP/s, gradient 17.9 ms, 1472; gated 8192 x
-// 4096 x 16384 with both projections kept 1.56 ms, 1405, gradient 3.31 ms, 1329 (the
-// library's plain product of 8192^3 1619, 1388 with b across the sum, 1204 with both):
-// bound by the board's power.
+// cycles a slab (its 128 MFMAs take 2048) and of the epilogue: logsumexp 2200 and 12680,
+// gated 2220 and 10010 (three outputs 2240 and 21000), dx 2220 and 8320, dW 2490 to 2690 and
+// 8570.  8192 x 4096 x 131072, over several cards: loss 5.54 to 5.98 ms, 1588 to 1470 TFLOP/s,
+// gradient 17.9 to 19.1 ms, 1478 to 1380; gated 8192 x 4096 x 16384 with both projections
+// kept 1.53 to 1.57 ms, 1436 to 1403, gradient 3.30 to 3.37 ms, 1332 to 1304 (the library's
+// plain product of 8192^3 1635, 1393 with b across the sum, 1217 with both): bound by the
+// board's power.
 #pragma once
 
 #include "tile_scheduler.h"
@@ -702,6 +703,8 @@ __global__ __launch_bounds__(256, T == 256 ? 1 : 2) void linear_kernel(LinArgs a
             if (lg == 0u && m < args.M) args.part[(size_t)(u.n_idx * 2u + wc) * args.M + m] = make_float2(all, s);
         }
     } else if constexpr (EPI == LIN_DLOGITS) {
+        // dl is rounded once to the 16 bits that the matrix core takes: dx and dweight, 1.7e-3 off
+        // in bf16 and 2.1e-4 in fp16 by their own rounding, become 1.8e-3 and 2.3e-4 off.
         const uint32_t c0 = n0 + wc * WT;
         auto gradient = [&](auto inside_c) __attribute__((always_inline)) {
             constexpr bool INSIDE = decltype(inside_c)::value;

@@ -81,7 +81,7 @@ inline int64_t gated_pitch(int64_t hidden) { return round_up(hidden, 256); }
 // 2048 or fewer; else as many pieces as there are of that size, made alike (40000 rows of
 // 2100 words: two of 1280).  At most 2^22 (32-bit offsets in a quarter of a slab).  A
 // piece that the Infinity Cache (256 MiB) holds is read by both products without going
-// to HBM again: 8192 x 4096 x 131072 bf16 18.3 ms; with 64, 256 and 512 MiB 19.5, 18.8 and 18.6.
+// to HBM again: 8192 x 4096 x 131072 bf16 17.9 ms; with 64, 256 and 512 MiB 19.2, 18.5 and 18.2.
 inline int64_t vocab_piece(int64_t rows, int64_t vocab) {
     const int64_t most = (int64_t(1) << 26) / (rows > 0 ? rows : 1) / 256 * 256;
     const int64_t all = round_up(vocab, 256), piece = most < 2048 ? 2048 : most < (1 << 22) ? most : 1 << 22;
