@@ -16,3 +16,5 @@ def test_all_of_c_is_zero():
     tsg.Plan(M, N, 0, "fp16", 256, 256, 64, 8, 2).run(A, B, C)
     for i in range(0, M, 1 << 16):
         assert not C[i: i + (1 << 16)].any(), i
+    del C
+    torch.cuda.empty_cache()

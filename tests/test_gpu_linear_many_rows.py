@@ -31,3 +31,5 @@ def test_more_rows_than_a_join_has_groups():
         assert ((lse[s] - want).abs() <= off).all() and torch.isfinite(lse[s]).all()
         hit = l.gather(1, target[s, None])[:, 0]
         assert ((loss[s] - (want - hit)).abs() <= 2 * off).all() and torch.isfinite(loss[s]).all()
+    del x
+    torch.cuda.empty_cache()
